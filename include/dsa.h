@@ -245,6 +245,96 @@ dsa_status dsa_indexer_kl_loss_selected(const dsa_attn_args *args, int B, int Lq
                                         const float *sel_scores, float *target, float *kl, void *stream);
 
 /*
+ * Norm and position rotation of query and key heads in one pass: what makes the
+ * indexer's e4m3 queries and keys, the attention's queries and the latent rows from
+ * the projections' outputs.  (The pages give no formula for this step; it is the
+ * ordinary norm of a head followed by the rotary embedding.)  Per head row x of D columns, in
+ * fp32:
+ *   z[i] = (x[i] - mean) * r * weight[i] + bias[i]  for i < norm_dim, z[i] = x[i] behind;
+ *          r = 1/sqrt(mean((x - mean)^2) + eps) over the norm_dim columns; for
+ *          DSA_NORM_RMS mean is 0 and there is no bias;
+ *   y = z with its pairs in columns [rot_start, rot_start + 2*n_freq) turned by the
+ *       angle pos * inv_freq[j]:  (a cos - b sin, b cos + a sin).  Pair j is
+ *       (rot_start + j, rot_start + n_freq + j), or (rot_start + 2j, rot_start + 2j + 1)
+ *       when interleaved.  The angle is reduced in 64 bits, so far positions are exact.
+ * x may be a slice of a wider buffer (strides in elements, columns contiguous); a stride
+ * of 0 reads the same rows again.  D, norm_dim, rot_start, the strides: multiples of 8;
+ * n_freq: a multiple of 8; 8 <= D <= 1024.  B * L and B * L * H below 2^31.
+ */
+typedef enum { DSA_NORM_NONE = 0, DSA_NORM_RMS = 1, DSA_NORM_LAYER = 2 } dsa_norm;
+
+typedef struct {
+    int B, L, H, D;
+    int64_t stride_b, stride_l, stride_h; /* of x, in elements, >= 0 */
+    const void *x;             /* bf16 [B, L, H, D] by strides */
+    int norm;                  /* dsa_norm */
+    int norm_dim;              /* leading columns that are normalised (ignored for DSA_NORM_NONE) */
+    float eps;                 /* >= 0 */
+    const void *weight;        /* [norm_dim] */
+    const void *bias;          /* [norm_dim] or NULL (DSA_NORM_LAYER only) */
+    int weight_bf16;           /* weight and bias in bf16; 0: fp32 */
+    int rot_start, n_freq;     /* n_freq = 0: no rotation */
+    int interleaved;
+    const float *inv_freq;     /* fp32 [n_freq], radians per position */
+    const int32_t *positions;  /* int32 [B, L], or NULL: q_offset + l */
+    int q_offset;
+} dsa_norm_rope_args;
+
+/*
+ * scale == NULL: out is bf16 [B, L, H, D], contiguous, y rounded once.
+ * Otherwise out is e4m3 [B, L, H, D] and scale fp32 [B, L], as the indexer takes them
+ *   (dsa_indexer_args q_I/q_scale, or k_I/k_scale with H = 1): scale = max(amax of |y|
+ *   over the token's heads, 1e-30) / 448, code = rne(y / scale).  A token with a NaN has a
+ *   NaN scale.
+ * out must not overlap x.
+ */
+dsa_status dsa_norm_rope(const dsa_norm_rope_args *args, void *out, float *scale, void *stream);
+
+/*
+ * Gradient of the bf16 form (the e4m3 rounding passes the gradient through unchanged).
+ *   dy: bf16 [B, L, H, D], contiguous; dx: bf16 [B, L, H, D], contiguous, one row for
+ *   each row read (the caller adds rows that a stride of 0 repeated);
+ *   dweight, dbias: fp32 [norm_dim] (dweight required unless DSA_NORM_NONE, dbias exactly
+ *   when bias is given).  Sums are taken in a fixed order: the same call gives the same bits.
+ *   workspace: dsa_norm_rope_bwd_workspace(args) bytes; its contents need not be initialised.
+ * dx must not overlap dy or x.
+ */
+dsa_status dsa_norm_rope_bwd(const dsa_norm_rope_args *args, const void *dy, void *dx, float *dweight,
+                             float *dbias, void *workspace, size_t workspace_bytes, void *stream);
+size_t dsa_norm_rope_bwd_workspace(const dsa_norm_rope_args *args);
+
+/*
+ * The latent cache in 4 bits (2.8 times smaller than bf16 at d_qk = 576, d_v = 512).
+ * Value columns are held in groups of 32 as integers q in -7..7 and one bf16 step:
+ *   step = max|x| / 7 rounded up to 5 significant bits, q = rne(x / step), value = q*step,
+ * which is exact in bf16.  The tail (columns behind d_v, the rotated ones) stays bf16.
+ * A group with its largest magnitude below 2^-100 is stored as zeros; one with a NaN, an
+ * infinity or a magnitude above 2^126 reads back as NaN.
+ *   codes:  u8 [B, Lk, d_v/2].  Nibble = q + 8.  With chunk c = col/64, part p = col/16%4,
+ *           word w = col/8%2 the 8 columns of a word lie in the 4 bytes (little-endian) at
+ *           p*(d_v/8) + c*8 + w*4, column e = col%8 in nibble e/2 + 4*(e%2), counted from
+ *           the low end;
+ *   scales: bf16 [B, Lk, d_v/32], the step of group g = col/32 at (g%2)*(d_v/64) + g/2;
+ *   tail:   bf16 [B, Lk, d_qk - d_v].
+ * (d_qk, d_v) in {(192, 128), (576, 512)}, as the attention; B * Lk below 2^31.
+ */
+typedef struct {
+    int B, Lk, d_qk, d_v;
+    void *codes, *scales, *tail;
+} dsa_kv4_cache;
+
+/*
+ * Stores kv (bf16 [B, L, d_qk]) in cache rows first .. first + L - 1 of each sequence, where
+ * first is start[b] (int32 [B]) or, with start == NULL, offset.  Rows outside [0, Lk) are
+ * not stored; every other cache row is left as it was.
+ */
+dsa_status dsa_kv4_write(const dsa_kv4_cache *cache, const void *kv, int L, const int32_t *start, int offset,
+                         void *stream);
+/* Reads the same rows back into kv as the values they stand for (rows outside [0, Lk): zeros). */
+dsa_status dsa_kv4_read(const dsa_kv4_cache *cache, void *kv, int L, const int32_t *start, int offset,
+                        void *stream);
+
+/*
  * Bytes of device workspace the entry point `op` needs for these sizes (0 = none).
  * For DSA_OP_FORWARD, DSA_OP_FORWARD_LOWMEM and DSA_OP_INDEXER_TOPK it assumes
  * H_I = 64, d_I = 128 and q_offset = Lk - Lq (decode, or a prefill chunk);

@@ -21,6 +21,7 @@ import torch
 __all__ = [
     "DSAError", "lib", "lib_path", "indexer_scores", "topk", "indexer_topk", "sparse_attn", "sparse_attn_noalloc",
     "forward", "indexer_kl_loss", "indexer_kl_loss_selected",
+    "norm_rope", "norm_rope_bwd", "kv4_cache", "kv4_write", "kv4_read",
     "workspace_size", "workspace_size_args", "status_string", "device_status", "selftest_wait_timeout", "version",
     "OP_TOPK", "OP_SPARSE_ATTN", "OP_FORWARD", "OP_INDEXER_TOPK", "OP_FORWARD_LOWMEM",
 ]
@@ -51,6 +52,20 @@ class AttnArgs(ctypes.Structure):
                 ("q", ctypes.c_void_p), ("kv", ctypes.c_void_p)]
 
 
+class NormRopeArgs(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int), ("L", ctypes.c_int), ("H", ctypes.c_int), ("D", ctypes.c_int),
+                ("stride_b", ctypes.c_int64), ("stride_l", ctypes.c_int64), ("stride_h", ctypes.c_int64),
+                ("x", ctypes.c_void_p), ("norm", ctypes.c_int), ("norm_dim", ctypes.c_int), ("eps", ctypes.c_float),
+                ("weight", ctypes.c_void_p), ("bias", ctypes.c_void_p), ("weight_bf16", ctypes.c_int),
+                ("rot_start", ctypes.c_int), ("n_freq", ctypes.c_int), ("interleaved", ctypes.c_int),
+                ("inv_freq", ctypes.c_void_p), ("positions", ctypes.c_void_p), ("q_offset", ctypes.c_int)]
+
+
+class Kv4Cache(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int), ("Lk", ctypes.c_int), ("d_qk", ctypes.c_int), ("d_v", ctypes.c_int),
+                ("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("tail", ctypes.c_void_p)]
+
+
 _lib = None
 
 
@@ -72,6 +87,12 @@ def lib():
         L.dsa_indexer_topk.argtypes = [ctypes.POINTER(IndexerArgs), I, P, P, P, Z, P]
         L.dsa_indexer_kl_loss.argtypes = [ctypes.POINTER(AttnArgs), I, I, I, P, I, P, P, P, P, P]
         L.dsa_indexer_kl_loss_selected.argtypes = [ctypes.POINTER(AttnArgs), I, I, I, P, I, P, P, P, P, P]
+        L.dsa_norm_rope.argtypes = [ctypes.POINTER(NormRopeArgs), P, P, P]
+        L.dsa_norm_rope_bwd.argtypes = [ctypes.POINTER(NormRopeArgs), P, P, P, P, P, Z, P]
+        L.dsa_norm_rope_bwd_workspace.argtypes = [ctypes.POINTER(NormRopeArgs)]
+        L.dsa_norm_rope_bwd_workspace.restype = ctypes.c_size_t
+        L.dsa_kv4_write.argtypes = [ctypes.POINTER(Kv4Cache), P, I, P, I, P]
+        L.dsa_kv4_read.argtypes = [ctypes.POINTER(Kv4Cache), P, I, P, I, P]
         L.dsa_workspace_size.argtypes = [I, I, I, I, I, I, I]
         L.dsa_workspace_size.restype = ctypes.c_size_t
         L.dsa_workspace_size_args.argtypes = [I, ctypes.POINTER(IndexerArgs), I, I, I]
@@ -82,6 +103,7 @@ def lib():
         L.dsa_selftest_wait_timeout.argtypes = [ctypes.c_uint32, P]
         for f in ("dsa_indexer_scores", "dsa_topk", "dsa_indexer_topk", "dsa_sparse_attn", "dsa_sparse_attn_noalloc",
                   "dsa_forward", "dsa_forward_timed", "dsa_indexer_kl_loss", "dsa_indexer_kl_loss_selected",
+                  "dsa_norm_rope", "dsa_norm_rope_bwd", "dsa_kv4_write", "dsa_kv4_read",
                   "dsa_device_status",
                   "dsa_selftest_wait_timeout", "dsa_version"):
             getattr(L, f).restype = ctypes.c_int
@@ -346,6 +368,178 @@ def indexer_kl_loss_selected(q, kv, indices, lse, sel_scores, d_v, scale, target
                                               _ptr(sel_scores), _ptr(target), _ptr(kl), _stream(stream)),
            "dsa_indexer_kl_loss_selected")
     return target, kl
+
+
+def _need_at(t, dtype, shape, name, device):
+    """_need, and on the same device as the call's other tensors."""
+    _need(t, dtype, shape, name)
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+
+
+def _on(device, stream, call):
+    """call(stream handle) with `device` current, and with what it allocates belonging to
+    the stream that it launches on (a workspace freed on return is then reused in that
+    stream's order)."""
+    if stream is None and device.index == torch.cuda.current_device():
+        return call(ctypes.c_void_p(torch.cuda.current_stream().cuda_stream))
+    if stream is not None and stream.device != device:
+        raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
+    with torch.cuda.device(device):
+        with torch.cuda.stream(stream if stream is not None else torch.cuda.current_stream(device)):
+            return call(ctypes.c_void_p(torch.cuda.current_stream().cuda_stream))
+
+
+_NORMS = {None: 0, "rms": 1, "layer": 2}
+
+
+def _norm_rope_args(x, inv_freq, weight, bias, norm, norm_dim, eps, rot_start, interleaved, positions, q_offset):
+    if not isinstance(x, torch.Tensor) or x.dtype != torch.bfloat16:
+        raise TypeError("x must be a bfloat16 torch.Tensor")
+    if x.dim() != 4:
+        raise ValueError(f"x: shape {tuple(x.shape)}, expected [B, L, H, D]")
+    if not x.is_cuda or (x.stride(3) != 1 and x.shape[3] > 1):
+        raise ValueError("x must be a CUDA tensor with contiguous columns")
+    if norm not in _NORMS:
+        raise ValueError(f"norm {norm!r}: expected None, 'rms' or 'layer'")
+    dev = x.device
+    B, L, H, D = x.shape
+    a = NormRopeArgs(B, L, H, D, x.stride(0), x.stride(1), x.stride(2), x.data_ptr())
+    a.norm, a.eps = _NORMS[norm], float(eps)
+    if norm is not None:
+        a.norm_dim = D if norm_dim is None else int(norm_dim)
+        wt = weight.dtype if isinstance(weight, torch.Tensor) and weight.dtype == torch.bfloat16 else torch.float32
+        _need_at(weight, wt, (a.norm_dim,), "weight", dev)
+        a.weight, a.weight_bf16 = weight.data_ptr(), int(wt == torch.bfloat16)
+        if bias is not None:
+            _need_at(bias, wt, (a.norm_dim,), "bias", dev)
+            a.bias = bias.data_ptr()
+    elif weight is not None or bias is not None or norm_dim is not None:
+        raise ValueError("weight, bias and norm_dim belong to a norm")
+    a.rot_start, a.interleaved, a.q_offset = int(rot_start), int(bool(interleaved)), int(q_offset)
+    if inv_freq is not None:
+        _need_at(inv_freq, torch.float32, (inv_freq.numel(),), "inv_freq", dev)
+        a.n_freq, a.inv_freq = inv_freq.numel(), inv_freq.data_ptr()
+    if positions is not None:
+        _need_at(positions, torch.int32, (B, L), "positions", dev)
+        a.positions = positions.data_ptr()
+    return a
+
+
+def norm_rope(x, inv_freq=None, *, weight=None, bias=None, norm=None, norm_dim=None, eps=1e-6, rot_start=0,
+              interleaved=False, positions=None, q_offset=0, e4m3=False, out=None, scale=None, stream=None):
+    """Norm of each head row of ``x`` (bf16 [B, L, H, D], any strides over B, L, H) over its
+    leading ``norm_dim`` columns (``norm``: None, "rms" or "layer"; weight and bias fp32 or
+    bf16), then the position rotation of columns [rot_start, rot_start + 2F) by the angles
+    position * ``inv_freq`` (fp32 [F]; positions int32 [B, L], or q_offset + l).
+
+    Returns bf16 [B, L, H, D]; with ``e4m3`` the pair (float8_e4m3fn [B, L, H, D], fp32
+    scale [B, L]) that the indexer takes.  ``out`` must not overlap ``x``.
+    """
+    a = _norm_rope_args(x, inv_freq, weight, bias, norm, norm_dim, eps, rot_start, interleaved, positions, q_offset)
+    dev, shape = x.device, tuple(x.shape)
+    out_t = torch.float8_e4m3fn if e4m3 else torch.bfloat16
+    if not e4m3 and scale is not None:
+        raise ValueError("scale belongs to the e4m3 output")
+
+    def call(st):
+        o, sc = out, scale
+        if o is None:
+            o = torch.empty(shape, dtype=out_t, device=dev)
+        else:
+            _need_at(o, torch.uint8 if e4m3 and o.dtype == torch.uint8 else out_t, shape, "out", dev)
+        if e4m3:
+            if sc is None:
+                sc = torch.empty(shape[:2], dtype=torch.float32, device=dev)
+            _need_at(sc, torch.float32, shape[:2], "scale", dev)
+        _check(lib().dsa_norm_rope(ctypes.byref(a), o.data_ptr(), _ptr(sc), st), "dsa_norm_rope")
+        return (o, sc) if e4m3 else o
+
+    return _on(dev, stream, call)
+
+
+def norm_rope_bwd(dy, x, inv_freq=None, *, weight=None, bias=None, norm=None, norm_dim=None, eps=1e-6, rot_start=0,
+                  interleaved=False, positions=None, q_offset=0, dx=None, dweight=None, dbias=None, workspace=None,
+                  stream=None):
+    """Gradient of norm_rope's bf16 output: (dx bf16 [B, L, H, D], dweight fp32 or None,
+    dbias fp32 or None) for ``dy`` bf16 [B, L, H, D]; the other arguments as in the forward."""
+    a = _norm_rope_args(x, inv_freq, weight, bias, norm, norm_dim, eps, rot_start, interleaved, positions, q_offset)
+    dev, shape = x.device, tuple(x.shape)
+    _need_at(dy, torch.bfloat16, shape, "dy", dev)
+
+    def call(st):
+        gx, gw, gb, ws = dx, dweight, dbias, workspace
+        if gx is None:
+            gx = torch.empty(shape, dtype=torch.bfloat16, device=dev)
+        _need_at(gx, torch.bfloat16, shape, "dx", dev)
+        if norm is not None:
+            if gw is None:
+                gw = torch.empty(a.norm_dim, dtype=torch.float32, device=dev)
+            _need_at(gw, torch.float32, (a.norm_dim,), "dweight", dev)
+            if gb is None and bias is not None:
+                gb = torch.empty(a.norm_dim, dtype=torch.float32, device=dev)
+            if gb is not None:
+                _need_at(gb, torch.float32, (a.norm_dim,), "dbias", dev)
+            if ws is None:
+                ws = torch.empty(max(16, lib().dsa_norm_rope_bwd_workspace(ctypes.byref(a))), dtype=torch.uint8,
+                                 device=dev)
+        nbytes = 0 if ws is None else ws.numel() * ws.element_size()
+        _check(lib().dsa_norm_rope_bwd(ctypes.byref(a), dy.data_ptr(), gx.data_ptr(), _ptr(gw), _ptr(gb), _ptr(ws),
+                                       nbytes, st), "dsa_norm_rope_bwd")
+        return gx, gw, gb
+
+    return _on(dev, stream, call)
+
+
+def kv4_cache(B, Lk, d_qk, d_v, device="cuda"):
+    """An empty 4-bit latent cache: (codes uint8 [B, Lk, d_v/2], scales bf16 [B, Lk, d_v/32],
+    tail bf16 [B, Lk, d_qk - d_v]).  Rows that nothing was stored in read as zeros."""
+    codes = torch.full((B, Lk, d_v // 2), 0x88, dtype=torch.uint8, device=device)
+    scales = torch.zeros(B, Lk, d_v // 32, dtype=torch.bfloat16, device=device)
+    return codes, scales, torch.zeros(B, Lk, d_qk - d_v, dtype=torch.bfloat16, device=device)
+
+
+def _kv4(codes, scales, tail):
+    if not isinstance(codes, torch.Tensor) or codes.dim() != 3:
+        raise ValueError("codes must be a torch.Tensor [B, Lk, d_v/2]")
+    B, Lk, half = codes.shape
+    dev = codes.device
+    _need(codes, torch.uint8, (B, Lk, half), "codes")
+    _need_at(scales, torch.bfloat16, (B, Lk, half // 16), "scales", dev)
+    _need_at(tail, torch.bfloat16, (B, Lk, tail.shape[-1]), "tail", dev)
+    return Kv4Cache(B, Lk, 2 * half + tail.shape[-1], 2 * half, codes.data_ptr(), scales.data_ptr(), tail.data_ptr())
+
+
+def kv4_write(kv, codes, scales, tail, start=None, offset=0, stream=None):
+    """Stores latent rows ``kv`` (bf16 [B, L, d_qk]) in rows first .. first + L - 1 of each
+    sequence of the 4-bit cache; first is ``start`` (int32 [B]) or ``offset``.  Rows outside
+    the cache are not stored; the cache's other rows stay as they were."""
+    c = _kv4(codes, scales, tail)
+    dev = codes.device
+    L = kv.shape[1]
+    _need_at(kv, torch.bfloat16, (c.B, L, c.d_qk), "kv", dev)
+    if start is not None:
+        _need_at(start, torch.int32, (c.B,), "start", dev)
+    _on(dev, stream, lambda st: _check(lib().dsa_kv4_write(ctypes.byref(c), kv.data_ptr(), L, _ptr(start),
+                                                           int(offset), st), "dsa_kv4_write"))
+
+
+def kv4_read(codes, scales, tail, L, start=None, offset=0, kv=None, stream=None):
+    """bf16 [B, L, d_qk]: rows first .. first + L - 1 of each sequence as the values the
+    4-bit cache holds (rows outside the cache: zeros)."""
+    c = _kv4(codes, scales, tail)
+    dev = codes.device
+    L = int(L)
+    if start is not None:
+        _need_at(start, torch.int32, (c.B,), "start", dev)
+
+    def call(st):
+        o = torch.empty(c.B, L, c.d_qk, dtype=torch.bfloat16, device=dev) if kv is None else kv
+        _need_at(o, torch.bfloat16, (c.B, L, c.d_qk), "kv", dev)
+        _check(lib().dsa_kv4_read(ctypes.byref(c), o.data_ptr(), L, _ptr(start), int(offset), st), "dsa_kv4_read")
+        return o
+
+    return _on(dev, stream, call)
 
 
 def device_status(clear: bool = True) -> int:

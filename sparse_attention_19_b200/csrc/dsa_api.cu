@@ -410,6 +410,75 @@ dsa_status run_indexer_kl(const dsa_attn_args* a, int B, int Lq, int Lk, const i
   return DSA_OK;
 }
 
+dsa_status check_norm_rope(const dsa_norm_rope_args* a) {
+  if (!a || !a->x || a->B <= 0 || a->L <= 0 || a->H <= 0 || a->D <= 0) return DSA_ERR_INVALID_ARG;
+  if (!aligned16(a->x) || a->stride_b < 0 || a->stride_l < 0 || a->stride_h < 0) return DSA_ERR_INVALID_ARG;
+  if (a->norm != DSA_NORM_NONE && a->norm != DSA_NORM_RMS && a->norm != DSA_NORM_LAYER) return DSA_ERR_INVALID_ARG;
+  if (a->norm != DSA_NORM_NONE) {
+    if (!a->weight || !aligned16(a->weight) || !aligned16(a->bias)) return DSA_ERR_INVALID_ARG;
+    if (a->norm_dim <= 0 || a->norm_dim > a->D) return DSA_ERR_INVALID_ARG;
+    if (!(a->eps >= 0.f) || !std::isfinite(a->eps)) return DSA_ERR_INVALID_ARG;
+  }
+  if (a->bias && a->norm != DSA_NORM_LAYER) return DSA_ERR_INVALID_ARG;
+  if (a->n_freq < 0 || a->rot_start < 0) return DSA_ERR_INVALID_ARG;
+  if (a->n_freq > 0) {
+    if (!a->inv_freq || !aligned16(a->inv_freq) || !aligned16(a->positions)) return DSA_ERR_INVALID_ARG;
+    if ((long long)a->rot_start + 2LL * a->n_freq > a->D) return DSA_ERR_INVALID_ARG;
+    if (!a->positions && (long long)a->q_offset + a->L > (1LL << 31) - 1) return DSA_ERR_INVALID_ARG;
+  }
+  if (a->D % 8 || a->D > 1024 || a->rot_start % 8 || a->n_freq % 8) return DSA_ERR_UNSUPPORTED;
+  if (a->norm != DSA_NORM_NONE && a->norm_dim % 8) return DSA_ERR_UNSUPPORTED;
+  if (a->stride_b % 8 || a->stride_l % 8 || a->stride_h % 8) return DSA_ERR_UNSUPPORTED;
+  if ((long long)a->B * a->L >= (1LL << 31) || (long long)a->B * a->L * a->H >= (1LL << 31))
+    return DSA_ERR_UNSUPPORTED;
+  return DSA_OK;
+}
+
+NormRopeParams norm_rope_params(const dsa_norm_rope_args* a) {
+  NormRopeParams p{};
+  p.L = a->L; p.H = a->H; p.D = a->D;
+  p.n_tokens = a->B * a->L;
+  p.norm = a->norm;
+  p.norm_dim = a->norm == DSA_NORM_NONE ? 0 : a->norm_dim;
+  p.eps = a->eps;
+  p.w_bf16 = a->weight_bf16 ? 1 : 0;
+  p.rot_start = a->rot_start; p.n_freq = a->n_freq;
+  p.interleaved = a->interleaved ? 1 : 0;
+  p.q_offset = a->q_offset;
+  p.stride_b = a->stride_b; p.stride_l = a->stride_l; p.stride_h = a->stride_h;
+  p.x = reinterpret_cast<const __nv_bfloat16*>(a->x);
+  p.w = a->weight; p.b = a->bias;
+  p.inv_freq = a->inv_freq;
+  p.positions = a->positions;
+  return p;
+}
+
+dsa_status check_kv4(const dsa_kv4_cache* c) {
+  if (!c || !c->codes || !c->scales || !c->tail || c->B <= 0 || c->Lk <= 0) return DSA_ERR_INVALID_ARG;
+  if (!aligned16(c->codes) || !aligned16(c->scales) || !aligned16(c->tail)) return DSA_ERR_INVALID_ARG;
+  if (!((c->d_qk == 576 && c->d_v == 512) || (c->d_qk == 192 && c->d_v == 128))) return DSA_ERR_UNSUPPORTED;
+  if ((long long)c->B * c->Lk >= (1LL << 31)) return DSA_ERR_UNSUPPORTED;
+  return DSA_OK;
+}
+
+dsa_status run_kv4(const dsa_kv4_cache* c, const void* in, void* out, int L, const int32_t* start, int offset,
+                   cudaStream_t st) {
+  const dsa_status s = check_kv4(c);
+  if (s != DSA_OK) return s;
+  if (L <= 0 || (!in && !out) || !aligned16(in) || !aligned16(out) || !aligned16(start)) return DSA_ERR_INVALID_ARG;
+  if ((long long)c->B * L >= (1LL << 31)) return DSA_ERR_UNSUPPORTED;
+  Kv4Params p{};
+  p.B = c->B; p.L = L; p.Lk = c->Lk; p.d_qk = c->d_qk; p.d_v = c->d_v;
+  p.offset = offset;
+  p.start = start;
+  p.in = reinterpret_cast<const __nv_bfloat16*>(in);
+  p.out = reinterpret_cast<__nv_bfloat16*>(out);
+  p.codes = reinterpret_cast<uint8_t*>(c->codes);
+  p.scales = reinterpret_cast<__nv_bfloat16*>(c->scales);
+  p.tail = reinterpret_cast<__nv_bfloat16*>(c->tail);
+  return (in ? launch_kv4_write(p, st) : launch_kv4_read(p, st)) == cudaSuccess ? DSA_OK : DSA_ERR_CUDA;
+}
+
 __global__ void wait_selftest_kernel(uint32_t limit) {
   __shared__ uint64_t bar;
   if (threadIdx.x == 0) {
@@ -506,6 +575,53 @@ dsa_status dsa_indexer_kl_loss_selected(const dsa_attn_args* args, int B, int Lq
   if (k < 1 || k > kMaxK) return DSA_ERR_UNSUPPORTED;
   return run_indexer_kl(args, B, Lq, Lk, indices, k, lse, nullptr, sel_scores, target, kl,
                         static_cast<cudaStream_t>(stream));
+}
+
+dsa_status dsa_norm_rope(const dsa_norm_rope_args* args, void* out, float* scale, void* stream) {
+  const dsa_status s = check_norm_rope(args);
+  if (s != DSA_OK) return s;
+  if (!out || !aligned16(out) || !aligned16(scale)) return DSA_ERR_INVALID_ARG;
+  NormRopeParams p = norm_rope_params(args);
+  if (scale) p.codes = reinterpret_cast<uint8_t*>(out);
+  else p.out = reinterpret_cast<__nv_bfloat16*>(out);
+  p.scale = scale;
+  return launch_norm_rope(p, sm_count(), static_cast<cudaStream_t>(stream)) == cudaSuccess ? DSA_OK : DSA_ERR_CUDA;
+}
+
+size_t dsa_norm_rope_bwd_workspace(const dsa_norm_rope_args* args) {
+  if (check_norm_rope(args) != DSA_OK || args->norm == DSA_NORM_NONE) return 0;
+  return (size_t)norm_rope_bwd_blocks(sm_count()) * args->norm_dim * (args->bias ? 2 : 1) * sizeof(float);
+}
+
+dsa_status dsa_norm_rope_bwd(const dsa_norm_rope_args* args, const void* dy, void* dx, float* dweight, float* dbias,
+                             void* workspace, size_t workspace_bytes, void* stream) {
+  const dsa_status s = check_norm_rope(args);
+  if (s != DSA_OK) return s;
+  if (!dy || !dx || !aligned16(dy) || !aligned16(dx)) return DSA_ERR_INVALID_ARG;
+  if (args->norm != DSA_NORM_NONE && (!dweight || (args->bias != nullptr) != (dbias != nullptr)))
+    return DSA_ERR_INVALID_ARG;
+  if (!aligned16(dweight) || !aligned16(dbias)) return DSA_ERR_INVALID_ARG;
+  const size_t need = dsa_norm_rope_bwd_workspace(args);
+  if (need && (!workspace || workspace_bytes < need || !aligned16(workspace))) return DSA_ERR_WORKSPACE;
+  NormRopeParams p = norm_rope_params(args);
+  p.dy = reinterpret_cast<const __nv_bfloat16*>(dy);
+  p.dx = reinterpret_cast<__nv_bfloat16*>(dx);
+  p.dw = dweight;
+  p.db = dbias;
+  p.part = reinterpret_cast<float*>(workspace);
+  return launch_norm_rope_bwd(p, sm_count(), static_cast<cudaStream_t>(stream)) == cudaSuccess ? DSA_OK
+                                                                                               : DSA_ERR_CUDA;
+}
+
+dsa_status dsa_kv4_write(const dsa_kv4_cache* cache, const void* kv, int L, const int32_t* start, int offset,
+                         void* stream) {
+  if (!kv) return DSA_ERR_INVALID_ARG;
+  return run_kv4(cache, kv, nullptr, L, start, offset, static_cast<cudaStream_t>(stream));
+}
+
+dsa_status dsa_kv4_read(const dsa_kv4_cache* cache, void* kv, int L, const int32_t* start, int offset, void* stream) {
+  if (!kv) return DSA_ERR_INVALID_ARG;
+  return run_kv4(cache, nullptr, kv, L, start, offset, static_cast<cudaStream_t>(stream));
 }
 
 size_t dsa_workspace_size_args(dsa_op op, const dsa_indexer_args* iargs, int k, int H, int d_v) {

@@ -130,6 +130,50 @@ size_t indexer_kl_smem_bytes(int d_qk);
 cudaError_t launch_indexer_kl(const KlParams& p, int d_qk, const CUtensorMap& tq, const CUtensorMap& tkv,
                               int grid_clusters, cudaStream_t stream);
 
+// ---------------------------------------------------------------- norm and rotation of heads
+struct NormRopeParams {
+  int L, H, D;            // tokens are (b, l) pairs, b = token / L
+  int n_tokens;           // B * L
+  int tokens_per_block;   // set by the launcher
+  int norm, norm_dim;     // dsa_norm; columns [0, norm_dim) are normalised
+  float eps;
+  int w_bf16;             // w and b in bf16 instead of fp32
+  int rot_start, n_freq;  // rotated columns [rot_start, rot_start + 2 n_freq)
+  int interleaved, q_offset;
+  long long stride_b, stride_l, stride_h;   // of x, in elements
+  const __nv_bfloat16* x;
+  const void* w;          // [norm_dim]
+  const void* b;          // [norm_dim] or null
+  const float* inv_freq;  // [n_freq]
+  const int32_t* positions;   // [B, L] or null: q_offset + l
+  __nv_bfloat16* out;     // [B, L, H, D] bf16 ...
+  uint8_t* codes;         // ... or e4m3 [B, L, H, D]
+  float* scale;           // and [B, L]
+  const __nv_bfloat16* dy;    // gradient: [B, L, H, D]
+  __nv_bfloat16* dx;      // [B, L, H, D]
+  float* part;            // [2 (w, b)][blocks][norm_dim]
+  float* dw;              // [norm_dim]
+  float* db;              // [norm_dim] (when b is given)
+};
+constexpr int kNormRopeBwdBlocksPerSm = 4;
+int norm_rope_bwd_blocks(int sms);   // most partial rows the gradient leaves
+cudaError_t launch_norm_rope(NormRopeParams p, int sms, cudaStream_t stream);
+cudaError_t launch_norm_rope_bwd(NormRopeParams p, int sms, cudaStream_t stream);
+
+// ---------------------------------------------------------------- 4-bit latent cache
+struct Kv4Params {
+  int B, L, Lk, d_qk, d_v;
+  int offset;             // cache row of row 0 when start is null
+  const int32_t* start;   // [B] or null
+  const __nv_bfloat16* in;    // write: [B, L, d_qk]
+  __nv_bfloat16* out;     // read: [B, L, d_qk]
+  uint8_t* codes;         // [B, Lk, d_v / 2]
+  __nv_bfloat16* scales;  // [B, Lk, d_v / 32]
+  __nv_bfloat16* tail;    // [B, Lk, d_qk - d_v]
+};
+cudaError_t launch_kv4_write(const Kv4Params& p, cudaStream_t stream);
+cudaError_t launch_kv4_read(const Kv4Params& p, cudaStream_t stream);
+
 // ---------------------------------------------------------------- misc
 // Error words of the kernel units (one per translation unit), and their union.
 cudaError_t read_indexer_error(uint32_t* value, bool clear);

@@ -1,0 +1,154 @@
+// kv4.cu -- the latent cache in 4 bits: storing rows and reading them back.
+//
+// A latent row has d_v value columns and a tail of d_qk - d_v (rotated) columns.  The
+// value columns are held in groups of 32 as integers q in -7..7 times one bf16 step:
+//   step = max|x| / 7 rounded up to 5 significant bits,   q = rne(x / step),
+//   value = q * step.
+// Rounding the step up keeps |x / step| <= 7 (nothing is clipped), and 5 bits of step
+// times 3 bits of q fit bf16's 8, so the value is exact in bf16 and a reader may feed it
+// to a bf16 matrix product unrounded.  The tail stays bf16: the rotation puts position
+// into it, which 4 bits would lose.
+// A group whose largest magnitude is below 2^-100 is stored as zeros; one that holds a
+// NaN, an infinity or a magnitude above 2^126 has a NaN step and reads back as NaN.
+//
+// Row layout, chosen for the attention's loader (one thread then holds 16 columns of
+// every 64-column chunk in consecutive bytes): nibble = q + 8; with chunk c = col / 64,
+// part p = col / 16 % 4, word w = col / 8 % 2, the 8 columns of a word sit in the 4 bytes
+// at p * (d_v / 8) + c * 8 + w * 4, column e of the word in nibble e / 2 + 4 * (e % 2).
+// The step of group g = col / 32 is entry (g % 2) * (d_v / 64) + g / 2.
+//
+// Both kernels are bound by HBM (1152 bytes in, 416 out for a 576-column row, or the
+// reverse): a thread holds 16 columns, so a warp reads and writes whole rows.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "dsa_internal.h"
+#include "ptx.cuh"
+
+namespace dsa {
+
+namespace {
+
+constexpr int kThreads = 256;
+constexpr float kTiny = 7.888609052210118e-31f;       // 2^-100
+constexpr uint32_t kHugeBits = 0x7e800000u;           // bits of 2^126
+
+// Row and column share of a thread: LANES threads of 16 columns per row.
+template <int DV>
+struct Share {
+  static constexpr int kLanes = DV / 16;
+  static constexpr int kRows = kThreads / kLanes;     // rows per block
+};
+
+// Cache row of input row (b, i), or -1 when it lies outside the cache.
+__device__ __forceinline__ long long cache_row(const Kv4Params& p, int b, int i) {
+  const long long r = (long long)(p.start ? __ldg(p.start + b) : p.offset) + i;
+  return r >= 0 && r < p.Lk ? (long long)b * p.Lk + r : -1;
+}
+
+template <int DV>
+__global__ void __launch_bounds__(kThreads) kv4_write_kernel(const Kv4Params p) {
+  using S = Share<DV>;
+  const int lane = threadIdx.x % S::kLanes;           // columns 16 lane .. 16 lane + 15
+  const int row = (int)blockIdx.x * S::kRows + threadIdx.x / S::kLanes;
+  griddep_launch_dependents();
+  griddep_wait();
+  const bool here = row < p.B * p.L;
+  const long long at = here ? cache_row(p, row / p.L, row % p.L) : -1;
+  const uint4* src = reinterpret_cast<const uint4*>(p.in + (size_t)(here ? row : 0) * p.d_qk);
+  uint4 v[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)}, t = v[0];
+  const int tail8 = (p.d_qk - DV) / 8;                // 16-byte vectors of the tail
+  if (at >= 0) {
+    v[0] = __ldg(src + 2 * lane);
+    v[1] = __ldg(src + 2 * lane + 1);
+    if (lane < tail8) t = __ldg(src + DV / 8 + lane);
+  }
+  const uint32_t w[8] = {v[0].x, v[0].y, v[0].z, v[0].w, v[1].x, v[1].y, v[1].z, v[1].w};
+  float x[16];
+  uint32_t m = 0;                                     // largest magnitude as an integer: a NaN wins
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    x[2 * i] = __uint_as_float(w[i] << 16);
+    x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    m = max(m, max((w[i] << 16) & 0x7fffffffu, w[i] & 0x7fff0000u));
+  }
+  m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));     // the group's other 16 columns
+  float step = __uint_as_float((__float_as_uint(__fdiv_rn(__uint_as_float(m), 7.f)) + 0x7ffffu) & ~0x7ffffu);
+  const bool zero = __uint_as_float(m) < kTiny, bad = m > kHugeBits;
+  if (zero) step = 0.f;
+  if (bad) step = __uint_as_float(0x7fc00000u);
+  uint32_t code[2] = {0x88888888u, 0x88888888u};
+  if (!zero && !bad) {
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      code[k] = 0;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const int q = __float2int_rn(__fdiv_rn(x[8 * k + e], step)) + 8;
+        code[k] |= (uint32_t)q << (4 * (e / 2 + 4 * (e % 2)));
+      }
+    }
+  }
+  if (at < 0) return;
+  const int c = lane / 4, part = lane % 4;
+  *reinterpret_cast<uint2*>(p.codes + (size_t)at * (DV / 2) + part * (DV / 8) + c * 8) = make_uint2(code[0], code[1]);
+  if (part % 2 == 0)
+    p.scales[(size_t)at * (DV / 32) + (part / 2) * (DV / 64) + c] = __float2bfloat16_rn(step);
+  if (lane < tail8) reinterpret_cast<uint4*>(p.tail + (size_t)at * (p.d_qk - DV))[lane] = t;
+}
+
+template <int DV>
+__global__ void __launch_bounds__(kThreads) kv4_read_kernel(const Kv4Params p) {
+  using S = Share<DV>;
+  const int lane = threadIdx.x % S::kLanes;
+  const int row = (int)blockIdx.x * S::kRows + threadIdx.x / S::kLanes;
+  griddep_launch_dependents();
+  griddep_wait();
+  if (row >= p.B * p.L) return;
+  const long long at = cache_row(p, row / p.L, row % p.L);
+  const int tail8 = (p.d_qk - DV) / 8, c = lane / 4, part = lane % 4;
+  uint32_t w[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+  uint4 t = make_uint4(0, 0, 0, 0);
+  if (at >= 0) {
+    const uint2 code = __ldg(reinterpret_cast<const uint2*>(p.codes + (size_t)at * (DV / 2) + part * (DV / 8) + c * 8));
+    const float step = __bfloat162float(p.scales[(size_t)at * (DV / 32) + (part / 2) * (DV / 64) + c]);
+    if (lane < tail8) t = __ldg(reinterpret_cast<const uint4*>(p.tail + (size_t)at * (p.d_qk - DV)) + lane);
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const uint32_t cw = k ? code.y : code.x;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {                   // columns 2i and 2i + 1 sit 4 nibbles apart
+        const float lo = (float)((int)((cw >> (4 * i)) & 15u) - 8) * step;
+        const float hi = (float)((int)((cw >> (4 * i + 16)) & 15u) - 8) * step;
+        const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
+        w[4 * k + i] = *reinterpret_cast<const uint32_t*>(&b);
+      }
+    }
+  }
+  uint4* dst = reinterpret_cast<uint4*>(p.out + (size_t)row * p.d_qk);
+  dst[2 * lane] = make_uint4(w[0], w[1], w[2], w[3]);
+  dst[2 * lane + 1] = make_uint4(w[4], w[5], w[6], w[7]);
+  if (lane < tail8) dst[DV / 8 + lane] = t;
+}
+
+unsigned blocks(const Kv4Params& p, int rows_per_block) {
+  return (unsigned)(((long long)p.B * p.L + rows_per_block - 1) / rows_per_block);
+}
+
+}  // namespace
+
+cudaError_t launch_kv4_write(const Kv4Params& p, cudaStream_t stream) {
+  if (p.d_v == 512)
+    return launch_pdl(kv4_write_kernel<512>, dim3(blocks(p, Share<512>::kRows)), dim3(kThreads), 0, stream, p);
+  return launch_pdl(kv4_write_kernel<128>, dim3(blocks(p, Share<128>::kRows)), dim3(kThreads), 0, stream, p);
+}
+
+cudaError_t launch_kv4_read(const Kv4Params& p, cudaStream_t stream) {
+  if (p.d_v == 512)
+    return launch_pdl(kv4_read_kernel<512>, dim3(blocks(p, Share<512>::kRows)), dim3(kThreads), 0, stream, p);
+  return launch_pdl(kv4_read_kernel<128>, dim3(blocks(p, Share<128>::kRows)), dim3(kThreads), 0, stream, p);
+}
+
+}  // namespace dsa

@@ -1,0 +1,156 @@
+"""The operators around the attention without a GPU: refusals on the host before
+anything is enqueued, the 64-bit forms the GPU tests compare with (the gradient
+against differences), and the 4-bit cache's layout."""
+import ctypes
+
+import pytest
+import torch
+
+import ref_ops as R
+import sparse_attention_19_b200 as dsa
+from sparse_attention_19_b200 import build as dsa_build
+
+
+@pytest.fixture(scope="module")
+def L():
+    dsa_build.build()
+    return dsa.lib()
+
+
+P = ctypes.c_void_p(16)
+ODD = ctypes.c_void_p(24)
+INVALID, UNSUPPORTED, WORKSPACE = 1, 2, 3
+
+
+def _nr(**kw):
+    base = dict(B=1, L=4, H=2, D=64, stride_b=512, stride_l=128, stride_h=64, x=16, norm=1, norm_dim=64, eps=1e-6,
+                weight=16, bias=None, weight_bf16=0, rot_start=0, n_freq=16, interleaved=0, inv_freq=16,
+                positions=None, q_offset=0)
+    base.update(kw)
+    return dsa.NormRopeArgs(**base)
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(x=None), INVALID), (dict(x=24), INVALID), (dict(B=0), INVALID), (dict(L=0), INVALID), (dict(H=0), INVALID),
+    (dict(D=0), INVALID), (dict(norm=3), INVALID), (dict(weight=None), INVALID), (dict(weight=24), INVALID),
+    (dict(norm_dim=0), INVALID), (dict(norm_dim=72), INVALID), (dict(eps=-1.0), INVALID),
+    (dict(eps=float("nan")), INVALID), (dict(bias=16), INVALID), (dict(norm=2, bias=24), INVALID),
+    (dict(n_freq=-8), INVALID), (dict(rot_start=-8), INVALID), (dict(inv_freq=None), INVALID),
+    (dict(inv_freq=24), INVALID), (dict(positions=24), INVALID), (dict(rot_start=40), INVALID),
+    (dict(stride_l=-128), INVALID), (dict(q_offset=2 ** 31 - 4), INVALID),
+    (dict(D=60), INVALID), (dict(D=60, norm_dim=56), UNSUPPORTED), (dict(D=1032), UNSUPPORTED), (dict(norm_dim=60), UNSUPPORTED),
+    (dict(n_freq=12), UNSUPPORTED), (dict(rot_start=4), UNSUPPORTED), (dict(stride_h=60), UNSUPPORTED),
+    (dict(B=2 ** 16, L=2 ** 15), UNSUPPORTED), (dict(B=2 ** 12, L=2 ** 12, H=2 ** 8), UNSUPPORTED),
+])
+def test_norm_rope_refuses(L, kw, status):
+    a = _nr(**kw)
+    assert L.dsa_norm_rope(ctypes.byref(a), P, None, None) == status
+    assert L.dsa_norm_rope(ctypes.byref(a), P, P, None) == status
+    assert L.dsa_norm_rope_bwd(ctypes.byref(a), P, P, P, P if a.bias else None, P, 1 << 30, None) == status
+    assert L.dsa_norm_rope_bwd_workspace(ctypes.byref(a)) == 0
+
+
+def test_norm_rope_refuses_outputs_and_workspace(L):
+    a = _nr()
+    assert L.dsa_norm_rope(None, P, None, None) == INVALID
+    assert L.dsa_norm_rope(ctypes.byref(a), None, None, None) == INVALID
+    assert L.dsa_norm_rope(ctypes.byref(a), ODD, None, None) == INVALID
+    assert L.dsa_norm_rope(ctypes.byref(a), P, ODD, None) == INVALID
+    need = L.dsa_norm_rope_bwd_workspace(ctypes.byref(a))
+    assert need > 0 and need % (64 * 4) == 0
+    layer = _nr(norm=2, bias=16)
+    assert L.dsa_norm_rope_bwd_workspace(ctypes.byref(layer)) == 2 * need
+    f = L.dsa_norm_rope_bwd
+    assert f(ctypes.byref(a), None, P, P, None, P, need, None) == INVALID
+    assert f(ctypes.byref(a), P, None, P, None, P, need, None) == INVALID
+    assert f(ctypes.byref(a), P, P, None, None, P, need, None) == INVALID          # no dweight
+    assert f(ctypes.byref(a), P, P, P, P, P, need, None) == INVALID                # dbias without a bias
+    assert f(ctypes.byref(layer), P, P, P, None, P, 2 * need, None) == INVALID     # a bias without dbias
+    assert f(ctypes.byref(a), P, P, P, None, P, need - 1, None) == WORKSPACE
+    assert f(ctypes.byref(a), P, P, P, None, None, need, None) == WORKSPACE
+    assert f(ctypes.byref(a), P, P, P, None, ODD, need, None) == WORKSPACE
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(B=0), INVALID), (dict(Lk=0), INVALID), (dict(codes=None), INVALID), (dict(scales=None), INVALID),
+    (dict(tail=None), INVALID), (dict(codes=24), INVALID), (dict(scales=24), INVALID), (dict(tail=24), INVALID),
+    (dict(d_qk=512), UNSUPPORTED), (dict(d_v=256), UNSUPPORTED), (dict(B=2 ** 16, Lk=2 ** 15), UNSUPPORTED),
+])
+def test_kv4_refuses(L, kw, status):
+    base = dict(B=2, Lk=8, d_qk=576, d_v=512, codes=16, scales=16, tail=16)
+    base.update(kw)
+    c = dsa.Kv4Cache(**base)
+    for f in (L.dsa_kv4_write, L.dsa_kv4_read):
+        assert f(ctypes.byref(c), P, 1, None, 0, None) == status
+
+
+def test_kv4_refuses_rows(L):
+    c = dsa.Kv4Cache(2, 8, 576, 512, 16, 16, 16)
+    for f in (L.dsa_kv4_write, L.dsa_kv4_read):
+        assert f(None, P, 1, None, 0, None) == INVALID
+        assert f(ctypes.byref(c), None, 1, None, 0, None) == INVALID
+        assert f(ctypes.byref(c), ODD, 1, None, 0, None) == INVALID
+        assert f(ctypes.byref(c), P, 0, None, 0, None) == INVALID
+        assert f(ctypes.byref(c), P, 1, ODD, 0, None) == INVALID
+        assert f(ctypes.byref(c), P, 2 ** 30, None, 0, None) == UNSUPPORTED
+
+
+def test_binding_refuses_tensors_that_are_not_on_a_gpu():
+    x = torch.zeros(1, 2, 3, 64, dtype=torch.bfloat16)
+    with pytest.raises(ValueError):
+        dsa.norm_rope(x)
+    with pytest.raises(TypeError):
+        dsa.norm_rope(x.float())
+    codes, scales, tail = dsa.kv4_cache(1, 4, 576, 512, device="cpu")
+    assert codes.shape == (1, 4, 256) and scales.shape == (1, 4, 16) and tail.shape == (1, 4, 64)
+    assert (R.kv4_values(codes, scales, tail) == 0).all()
+    with pytest.raises(ValueError):
+        dsa.kv4_read(codes, scales, tail, 1)
+
+
+@pytest.mark.parametrize("kind", ["rms", "layer", None])
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_gradient_form_against_differences(kind, interleaved):
+    g = torch.Generator().manual_seed(5)
+    x, dy, v = (torch.randn(2, 3, 2, 32, generator=g, dtype=torch.float64) for _ in range(3))
+    nd, rs = 24, 8
+    w, wv = (1 + 0.3 * torch.randn(nd, generator=g, dtype=torch.float64) for _ in range(2))
+    b, bv = (torch.randn(nd, generator=g, dtype=torch.float64) for _ in range(2)) if kind == "layer" else (None, None)
+    pos = torch.tensor([[0, 1, 7], [100000, 100001, 3]])
+    inv = torch.tensor([1.0, 0.3, 0.1, 0.03, 0.01, 0.003, 0.001, 0.0003])
+    how = dict(kind=kind, norm_dim=nd, rot_start=rs, interleaved=interleaved)
+
+    def f(h):
+        bias = None if b is None else b + h * bv
+        y, _ = R.norm_rope(x + h * v, pos, inv, w + h * wv, bias, **how)
+        return (y * dy).sum()
+
+    dx, dw, db, _ = R.norm_rope_bwd(dy, x, pos, inv, w, b, **how)
+    want = (dx * v).sum()
+    if kind is not None:
+        want = want + (dw * wv).sum() + (0 if b is None else (db * bv).sum())
+    # central difference: error h^2/6 f''' ~ 1e-8, rounding 1e-16/h * |f| ~ 1e-10
+    h = 1e-4
+    assert abs((f(h) - f(-h)) / (2 * h) - want) < 1e-5 * (1 + abs(want))
+
+
+@pytest.mark.parametrize("d_v", [128, 512])
+def test_kv4_layout_holds_every_column_once(d_v):
+    seen = {R.kv4_nibble(d_v, c) for c in range(d_v)}
+    assert seen == {(b, s) for b in range(d_v // 2) for s in (0, 4)}
+    slots = {}
+    for c in range(d_v):
+        slots.setdefault(R.kv4_scale_slot(d_v, c), set()).add(c // 32)
+    assert sorted(slots) == list(range(d_v // 32)) and all(len(g) == 1 for g in slots.values())
+
+
+def test_kv4_values_are_exact_in_bf16():
+    g = torch.Generator().manual_seed(1)
+    kv = (torch.randn(64, 576, generator=g) * torch.logspace(-20, 20, 64)[:, None]).bfloat16()
+    v, step = R.kv4_quantised(kv, 512)
+    assert torch.equal(v.bfloat16().double(), v)
+    assert torch.equal(step.bfloat16().double(), step)
+    # nothing is clipped, and no value is off by more than half a step
+    x = kv[:, :512].double().unflatten(-1, (-1, 32))
+    off = (v[:, :512].unflatten(-1, (-1, 32)) - x).abs()
+    assert (off <= step.unsqueeze(-1) / 2).all()
