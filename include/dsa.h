@@ -75,7 +75,8 @@ typedef enum {
     DSA_OP_SPARSE_ATTN = 1,
     DSA_OP_FORWARD = 2,          /* dsa_forward, staged selection (the faster path) */
     DSA_OP_INDEXER_TOPK = 3,
-    DSA_OP_FORWARD_LOWMEM = 4    /* dsa_forward, fused selection (no score matrix) */
+    DSA_OP_FORWARD_LOWMEM = 4,   /* dsa_forward, fused selection (no score matrix) */
+    DSA_OP_WINDOW_ATTN = 5       /* dsa_window_attn; k = window + sinks (of any size) */
 } dsa_op;
 
 /*
@@ -333,6 +334,45 @@ dsa_status dsa_kv4_write(const dsa_kv4_cache *cache, const void *kv, int L, cons
 /* Reads the same rows back into kv as the values they stand for (rows outside [0, Lk): zeros). */
 dsa_status dsa_kv4_read(const dsa_kv4_cache *cache, void *kv, int L, const int32_t *start, int offset,
                         void *stream);
+
+/*
+ * dsa_sparse_attn over the 4-bit cache: the same attention with c_s as the cache holds it
+ * (its values are exact in bf16, so nothing is rounded on the way to the matrix product).
+ *   indices, k, out, lse, workspace (DSA_OP_SPARSE_ATTN), limits: as dsa_sparse_attn.  Rows of
+ *   the cache that no valid entry names are not read, so they may hold anything.
+ */
+typedef struct {
+    int H, d_qk, d_v;
+    float scale;
+    const void *q;                       /* bf16 [B, Lq, H, d_qk] */
+    const void *codes, *scales, *tail;   /* dsa_kv4_cache arrays of [B, Lk, ...] */
+} dsa_kv4_attn_args;
+dsa_status dsa_sparse_attn_kv4(const dsa_kv4_attn_args *args, int B, int Lq, int Lk, const int32_t *indices, int k,
+                               void *out, float *lse, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * dsa_forward with the latent rows in the 4-bit cache (the indexer's keys stay e4m3).
+ *   sel_scores: as dsa_forward_timed (may be NULL); workspace: as dsa_forward (DSA_OP_FORWARD
+ *   or DSA_OP_FORWARD_LOWMEM); short sequences as there.
+ */
+dsa_status dsa_forward_kv4(const dsa_indexer_args *iargs, const dsa_kv4_attn_args *kargs, int k, int32_t *indices,
+                           float *sel_scores, void *out, float *lse, void *workspace, size_t workspace_bytes,
+                           void *stream);
+
+/*
+ * MLA attention with a sliding window and sinks, for layers without a selection (the pages
+ * have no counterpart; same q, kv, out and lse as dsa_sparse_attn).
+ *   Query i of sequence b sits at t = (start ? start[b] : q_offset) + i and sees the keys
+ *   s with t - window < s <= t, and the first `sinks` keys s < sinks, s <= t; of either only
+ *   those in [0, Lk).  start: int32 [B], sequences of different lengths (any values; a
+ *   query that sees nothing gets out = 0, lse = -INFINITY).  Keys that no query sees are
+ *   not read into a result: they may hold anything.
+ *   1 <= window, 0 <= sinks, Lq <= Lk; without start q_offset + Lq <= Lk.
+ *   workspace: dsa_workspace_size(DSA_OP_WINDOW_ATTN, B, Lq, Lk, window + sinks, H, d_v).
+ */
+dsa_status dsa_window_attn(const dsa_attn_args *args, int B, int Lq, int Lk, int q_offset, const int32_t *start,
+                           int window, int sinks, void *out, float *lse, void *workspace, size_t workspace_bytes,
+                           void *stream);
 
 /*
  * Bytes of device workspace the entry point `op` needs for these sizes (0 = none).

@@ -21,15 +21,16 @@ import torch
 __all__ = [
     "DSAError", "lib", "lib_path", "indexer_scores", "topk", "indexer_topk", "sparse_attn", "sparse_attn_noalloc",
     "forward", "indexer_kl_loss", "indexer_kl_loss_selected",
-    "norm_rope", "norm_rope_bwd", "kv4_cache", "kv4_write", "kv4_read",
+    "norm_rope", "norm_rope_bwd", "kv4_cache", "kv4_write", "kv4_read", "sparse_attn_kv4", "forward_kv4",
+    "window_attn",
     "workspace_size", "workspace_size_args", "status_string", "device_status", "selftest_wait_timeout", "version",
-    "OP_TOPK", "OP_SPARSE_ATTN", "OP_FORWARD", "OP_INDEXER_TOPK", "OP_FORWARD_LOWMEM",
+    "OP_TOPK", "OP_SPARSE_ATTN", "OP_FORWARD", "OP_INDEXER_TOPK", "OP_FORWARD_LOWMEM", "OP_WINDOW_ATTN",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 lib_path = os.path.join(_HERE, "libdsa.so")
 
-OP_TOPK, OP_SPARSE_ATTN, OP_FORWARD, OP_INDEXER_TOPK, OP_FORWARD_LOWMEM = 0, 1, 2, 3, 4
+OP_TOPK, OP_SPARSE_ATTN, OP_FORWARD, OP_INDEXER_TOPK, OP_FORWARD_LOWMEM, OP_WINDOW_ATTN = 0, 1, 2, 3, 4, 5
 _STATUS = {0: "DSA_OK", 1: "DSA_ERR_INVALID_ARG", 2: "DSA_ERR_UNSUPPORTED", 3: "DSA_ERR_WORKSPACE",
            4: "DSA_ERR_CUDA", 5: "DSA_ERR_TIMEOUT"}
 
@@ -66,6 +67,12 @@ class Kv4Cache(ctypes.Structure):
                 ("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("tail", ctypes.c_void_p)]
 
 
+class Kv4AttnArgs(ctypes.Structure):
+    _fields_ = [("H", ctypes.c_int), ("d_qk", ctypes.c_int), ("d_v", ctypes.c_int), ("scale", ctypes.c_float),
+                ("q", ctypes.c_void_p), ("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p),
+                ("tail", ctypes.c_void_p)]
+
+
 _lib = None
 
 
@@ -93,6 +100,9 @@ def lib():
         L.dsa_norm_rope_bwd_workspace.restype = ctypes.c_size_t
         L.dsa_kv4_write.argtypes = [ctypes.POINTER(Kv4Cache), P, I, P, I, P]
         L.dsa_kv4_read.argtypes = [ctypes.POINTER(Kv4Cache), P, I, P, I, P]
+        L.dsa_sparse_attn_kv4.argtypes = [ctypes.POINTER(Kv4AttnArgs), I, I, I, P, I, P, P, P, Z, P]
+        L.dsa_forward_kv4.argtypes = [ctypes.POINTER(IndexerArgs), ctypes.POINTER(Kv4AttnArgs), I, P, P, P, P, P, Z, P]
+        L.dsa_window_attn.argtypes = [ctypes.POINTER(AttnArgs), I, I, I, I, P, I, I, P, P, P, Z, P]
         L.dsa_workspace_size.argtypes = [I, I, I, I, I, I, I]
         L.dsa_workspace_size.restype = ctypes.c_size_t
         L.dsa_workspace_size_args.argtypes = [I, ctypes.POINTER(IndexerArgs), I, I, I]
@@ -104,6 +114,7 @@ def lib():
         for f in ("dsa_indexer_scores", "dsa_topk", "dsa_indexer_topk", "dsa_sparse_attn", "dsa_sparse_attn_noalloc",
                   "dsa_forward", "dsa_forward_timed", "dsa_indexer_kl_loss", "dsa_indexer_kl_loss_selected",
                   "dsa_norm_rope", "dsa_norm_rope_bwd", "dsa_kv4_write", "dsa_kv4_read",
+                  "dsa_sparse_attn_kv4", "dsa_forward_kv4", "dsa_window_attn",
                   "dsa_device_status",
                   "dsa_selftest_wait_timeout", "dsa_version"):
             getattr(L, f).restype = ctypes.c_int
@@ -538,6 +549,94 @@ def kv4_read(codes, scales, tail, L, start=None, offset=0, kv=None, stream=None)
         _need_at(o, torch.bfloat16, (c.B, L, c.d_qk), "kv", dev)
         _check(lib().dsa_kv4_read(ctypes.byref(c), o.data_ptr(), L, _ptr(start), int(offset), st), "dsa_kv4_read")
         return o
+
+    return _on(dev, stream, call)
+
+
+def _kv4_attn_args(q, codes, scales, tail, scale):
+    c = _kv4(codes, scales, tail)
+    B, Lq, H, D = q.shape
+    _need_at(q, torch.bfloat16, (c.B, Lq, H, c.d_qk), "q", codes.device)
+    return c, Kv4AttnArgs(H, c.d_qk, c.d_v, float(scale), q.data_ptr(), c.codes, c.scales, c.tail)
+
+
+def _attn_outputs(B, Lq, H, d_v, out, lse, want_lse, device):
+    if out is None:
+        out = torch.empty(B, Lq, H, d_v, dtype=torch.bfloat16, device=device)
+    else:
+        _need_at(out, torch.bfloat16, (B, Lq, H, d_v), "out", device)
+    if lse is None and want_lse:
+        lse = torch.empty(B, Lq, H, dtype=torch.float32, device=device)
+    elif lse is not None:
+        _need_at(lse, torch.float32, (B, Lq, H), "lse", device)
+    return out, lse
+
+
+def sparse_attn_kv4(q, codes, scales, tail, indices, scale, out=None, lse=None, want_lse=True, workspace=None,
+                    stream=None):
+    """sparse_attn over the rows of a 4-bit cache (kv4_cache): bf16 [B, Lq, H, d_v] and fp32
+    lse [B, Lq, H].  Rows that ``indices`` does not name may hold anything."""
+    c, a = _kv4_attn_args(q, codes, scales, tail, scale)
+    dev, Lq, k = q.device, q.shape[1], indices.shape[-1]
+    _need_at(indices, torch.int32, (c.B, Lq, k), "indices", dev)
+
+    def call(st):
+        o, l = _attn_outputs(c.B, Lq, a.H, c.d_v, out, lse, want_lse, dev)
+        ws, nbytes = _workspace(OP_SPARSE_ATTN, c.B, Lq, max(c.Lk, Lq), k, a.H, c.d_v, dev, workspace)
+        _check(lib().dsa_sparse_attn_kv4(ctypes.byref(a), c.B, Lq, c.Lk, _ptr(indices), k, _ptr(o), _ptr(l), _ptr(ws),
+                                         nbytes, st), "dsa_sparse_attn_kv4")
+        return o, l
+
+    return _on(dev, stream, call)
+
+
+def forward_kv4(q_I, q_scale, w, k_I, k_scale, q, codes, scales, tail, k, scale, q_offset=0, indices=None, out=None,
+                lse=None, want_lse=True, workspace=None, stream=None, sel_scores=None, low_memory=False):
+    """forward with the latent rows in a 4-bit cache.  Returns (indices, out, lse)."""
+    c, a = _kv4_attn_args(q, codes, scales, tail, scale)
+    dev = q.device
+    ia = _indexer_args(q_I, q_scale, w, k_I, k_scale, q_offset)
+    if (ia.B, ia.Lq, ia.Lk) != (c.B, q.shape[1], c.Lk) or w.device != dev:
+        raise ValueError(f"the indexer's B, Lq, Lk {(ia.B, ia.Lq, ia.Lk)} on {w.device} differ from the attention's "
+                         f"{(c.B, q.shape[1], c.Lk)} on {dev}")
+    if sel_scores is not None:
+        _need_at(sel_scores, torch.float32, (ia.B, ia.Lq, k), "sel_scores", dev)
+
+    def call(st):
+        i = torch.empty(ia.B, ia.Lq, k, dtype=torch.int32, device=dev) if indices is None else indices
+        _need_at(i, torch.int32, (ia.B, ia.Lq, k), "indices", dev)
+        o, l = _attn_outputs(ia.B, ia.Lq, a.H, c.d_v, out, lse, want_lse, dev)
+        ws, nbytes = _workspace(OP_FORWARD_LOWMEM if low_memory else OP_FORWARD, ia.B, ia.Lq, ia.Lk, k, a.H, c.d_v,
+                                dev, workspace, ia=ia)
+        _check(lib().dsa_forward_kv4(ctypes.byref(ia), ctypes.byref(a), int(k), _ptr(i), _ptr(sel_scores), _ptr(o),
+                                     _ptr(l), _ptr(ws), nbytes, st), "dsa_forward_kv4")
+        return i, o, l
+
+    return _on(dev, stream, call)
+
+
+def window_attn(q, kv, d_v, scale, window, sinks=0, q_offset=0, start=None, out=None, lse=None, want_lse=True,
+                workspace=None, stream=None):
+    """MLA attention where query i of sequence b, at t = (start[b] or q_offset) + i, sees the
+    keys (t - window, t] and the first ``sinks`` ones: bf16 [B, Lq, H, d_v] and fp32 lse
+    [B, Lq, H].  ``start``: int32 [B], any values; a query that sees nothing gets out = 0 and
+    lse = -inf.  Keys that no query sees may hold anything."""
+    a = _attn_args(q, kv, d_v, scale)
+    dev = q.device
+    B, Lq, H, _ = q.shape
+    Lk = kv.shape[1]
+    if kv.device != dev:
+        raise ValueError(f"kv is on {kv.device}, expected {dev}")
+    if start is not None:
+        _need_at(start, torch.int32, (B,), "start", dev)
+    window, sinks = min(int(window), 2 ** 31 - 1), min(int(sinks), 2 ** 31 - 1)
+
+    def call(st):
+        o, l = _attn_outputs(B, Lq, H, int(d_v), out, lse, want_lse, dev)
+        ws, nbytes = _workspace(OP_WINDOW_ATTN, B, Lq, Lk, min(window + sinks, Lk), H, int(d_v), dev, workspace)
+        _check(lib().dsa_window_attn(ctypes.byref(a), B, Lq, Lk, int(q_offset), _ptr(start), window, sinks, _ptr(o),
+                                     _ptr(l), _ptr(ws), nbytes, st), "dsa_window_attn")
+        return o, l
 
     return _on(dev, stream, call)
 

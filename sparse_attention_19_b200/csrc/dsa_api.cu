@@ -383,6 +383,72 @@ dsa_status run_attn(const dsa_attn_args* a, int B, int Lq, int Lk, int q_offset,
   return DSA_OK;
 }
 
+// Split, workspace and launch of the attention over the 4-bit cache (kv null) and of the
+// sliding window over bf16 rows kv; `p` holds the mode's own fields and n_tiles.
+dsa_status launch_attn_mode(AttnParams p, const void* q, const void* kv, int d_qk, int d_v, float scale, void* out,
+                            float* lse, void* ws, size_t ws_bytes, cudaStream_t st) {
+  const int rows = p.B * p.Lq;
+  p.splits = attn_splits(rows, p.n_tiles);
+  p.tiles_per_split = (p.n_tiles + p.splits - 1) / p.splits;
+  p.n_units = rows * p.splits;
+  p.scale_log2 = scale * 1.4426950408889634f;
+  p.out = reinterpret_cast<__nv_bfloat16*>(out);
+  p.lse = lse;
+  if (p.splits > 1) {
+    const size_t need = attn_ws_bytes(p.B, p.Lq, p.n_tiles * kAttnTile, p.H, d_v);
+    if (!ws || ws_bytes < need || !aligned16(ws)) return DSA_ERR_WORKSPACE;
+    const size_t per = (size_t)rows * p.splits * p.H;
+    p.part_o = reinterpret_cast<float*>(ws);
+    p.part_lse = reinterpret_cast<float*>(static_cast<char*>(ws) + round_up(per * d_v * 4, 256));
+  }
+  CUtensorMap tq;
+  if (!make_tmap(&tq, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, q, (uint64_t)rows * p.H, d_qk, 64, 64,
+                 CU_TENSOR_MAP_SWIZZLE_128B))
+    return DSA_ERR_CUDA;
+  CUtensorMap tkv = tq, tbox = tq;                         // single rows (gathers), 16 consecutive rows
+  if (kv && (!make_tmap(&tkv, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, kv, (uint64_t)p.B * p.Lk, d_qk, 64, 1,
+                        CU_TENSOR_MAP_SWIZZLE_128B) ||
+             !make_tmap(&tbox, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, kv, (uint64_t)p.B * p.Lk, d_qk, 64, 16,
+                        CU_TENSOR_MAP_SWIZZLE_128B)))
+    return DSA_ERR_CUDA;
+  const int pairs = sm_count() / 2;
+  const int grid = p.n_units < pairs ? p.n_units : pairs;
+  if (launch_sparse_attn(p, d_qk, d_v, tq, tkv, tbox, grid, st) != cudaSuccess) return DSA_ERR_CUDA;
+  if (p.splits > 1 && launch_attn_combine(p, d_v, st) != cudaSuccess) return DSA_ERR_CUDA;
+  return DSA_OK;
+}
+
+// Attention over the 4-bit cache; `dense_idx_out` as in run_attn.
+dsa_status run_attn_kv4(const dsa_kv4_attn_args* a, int B, int Lq, int Lk, int q_offset, bool compact,
+                        const int32_t* idx, int k, void* out, float* lse, void* ws, size_t ws_bytes, cudaStream_t st,
+                        int32_t* dense_idx_out = nullptr) {
+  AttnParams p{};
+  p.B = B; p.Lq = Lq; p.Lk = Lk; p.H = a->H; p.k = k;
+  p.dense = dense_idx_out ? 1 : 0;
+  p.idx_out = dense_idx_out;
+  p.compact = compact || dense_idx_out ? 1 : 0;
+  p.q_offset = q_offset;
+  p.indices = idx;
+  p.n_tiles = (k + kAttnTile - 1) / kAttnTile;
+  p.codes = reinterpret_cast<const uint8_t*>(a->codes);
+  p.scales = reinterpret_cast<const __nv_bfloat16*>(a->scales);
+  p.tail = reinterpret_cast<const __nv_bfloat16*>(a->tail);
+  return launch_attn_mode(p, a->q, nullptr, a->d_qk, a->d_v, a->scale, out, lse, ws, ws_bytes, st);
+}
+
+dsa_status check_kv4_attn(const dsa_kv4_attn_args* a, int B, int Lq, int Lk) {
+  if (!a || !a->codes || !a->scales || !a->tail) return DSA_ERR_INVALID_ARG;
+  if (!aligned16(a->codes) || !aligned16(a->scales) || !aligned16(a->tail)) return DSA_ERR_INVALID_ARG;
+  const dsa_attn_args b{a->H, a->d_qk, a->d_v, a->scale, a->q, a->codes};
+  return check_attn(&b, B, Lq, Lk);
+}
+
+// Slots of the longest row of a window: what it could see of Lk keys.
+int window_slots(int Lk, int window, int sinks) {
+  const long long n = (long long)window + sinks;
+  return n < Lk ? (int)n : Lk;
+}
+
 dsa_status run_indexer_kl(const dsa_attn_args* a, int B, int Lq, int Lk, const int32_t* indices, int k,
                           const float* lse, const float* scores, const float* sel_scores, float* target, float* kl,
                           cudaStream_t st) {
@@ -552,6 +618,35 @@ dsa_status dsa_sparse_attn(const dsa_attn_args* args, int B, int Lq, int Lk, con
                   static_cast<cudaStream_t>(stream));
 }
 
+dsa_status dsa_sparse_attn_kv4(const dsa_kv4_attn_args* args, int B, int Lq, int Lk, const int32_t* indices, int k,
+                               void* out, float* lse, void* workspace, size_t workspace_bytes, void* stream) {
+  const dsa_status s = check_kv4_attn(args, B, Lq, Lk);
+  if (s != DSA_OK) return s;
+  if (!indices || !out || !aligned16(indices) || !aligned16(out) || !aligned16(lse)) return DSA_ERR_INVALID_ARG;
+  if (k < 1 || k > kMaxK) return DSA_ERR_UNSUPPORTED;
+  return run_attn_kv4(args, B, Lq, Lk, 0, false, indices, k, out, lse, workspace, workspace_bytes,
+                      static_cast<cudaStream_t>(stream));
+}
+
+dsa_status dsa_window_attn(const dsa_attn_args* args, int B, int Lq, int Lk, int q_offset, const int32_t* start,
+                           int window, int sinks, void* out, float* lse, void* workspace, size_t workspace_bytes,
+                           void* stream) {
+  const dsa_status s = check_attn(args, B, Lq, Lk);
+  if (s != DSA_OK) return s;
+  if (!out || !aligned16(out) || !aligned16(lse) || !aligned16(start)) return DSA_ERR_INVALID_ARG;
+  if (window < 1 || sinks < 0 || Lq > Lk) return DSA_ERR_INVALID_ARG;
+  if (!start && (q_offset < 0 || (long long)q_offset + Lq > Lk)) return DSA_ERR_INVALID_ARG;
+  AttnParams p{};
+  p.B = B; p.Lq = Lq; p.Lk = Lk; p.H = args->H;
+  p.q_offset = q_offset;
+  p.start = start;
+  p.window = window;
+  p.sinks = sinks;
+  p.n_tiles = (window_slots(Lk, window, sinks) + kAttnTile - 1) / kAttnTile;
+  return launch_attn_mode(p, args->q, args->kv, args->d_qk, args->d_v, args->scale, out, lse, workspace,
+                          workspace_bytes, static_cast<cudaStream_t>(stream));
+}
+
 dsa_status dsa_indexer_kl_loss(const dsa_attn_args* args, int B, int Lq, int Lk, const int32_t* indices, int k,
                                const float* lse, const float* scores, float* target, float* kl, void* stream) {
   dsa_status s = check_attn(args, B, Lq, Lk);
@@ -641,13 +736,19 @@ size_t dsa_workspace_size_args(dsa_op op, const dsa_indexer_args* iargs, int k, 
       const size_t sel = indexer_topk_ws_bytes(iargs, k);
       return sel ? round_up(sel, 256) + attn_ws_bytes(iargs->B, iargs->Lq, k, H, d_v) : 0;
     }
+    case DSA_OP_WINDOW_ATTN:
+      break;
   }
   return 0;
 }
 
 size_t dsa_workspace_size(dsa_op op, int B, int Lq, int Lk, int k, int H, int d_v) {
-  if (B <= 0 || Lq <= 0 || Lk <= 0 || Lq > Lk || k < 1 || k > kMaxK || H <= 0 || d_v <= 0) return 0;
+  if (B <= 0 || Lq <= 0 || Lk <= 0 || Lq > Lk || k < 1 || H <= 0 || d_v <= 0) return 0;
+  if (op == DSA_OP_WINDOW_ATTN) return attn_ws_bytes(B, Lq, k < Lk ? k : Lk, H, d_v);
+  if (k > kMaxK) return 0;
   switch (op) {
+    case DSA_OP_WINDOW_ATTN:
+      break;
     case DSA_OP_TOPK:
       return 0;
     case DSA_OP_SPARSE_ATTN:
@@ -675,18 +776,25 @@ dsa_status dsa_indexer_topk(const dsa_indexer_args* args, int k, int32_t* indice
                           static_cast<cudaStream_t>(stream));
 }
 
-dsa_status dsa_forward_timed(const dsa_indexer_args* iargs, const dsa_attn_args* aargs, int k, int32_t* indices,
-                             float* sel_scores, void* out, float* lse, void* workspace, size_t workspace_bytes,
-                             void* stream, void* const* stage_events) {
+}  // extern "C"
+
+namespace {
+
+// Indexer, selection and one of the attentions: bf16 latent rows (aargs) or the 4-bit
+// cache (kargs).
+dsa_status forward(const dsa_indexer_args* iargs, const dsa_attn_args* aargs, const dsa_kv4_attn_args* kargs, int k,
+                   int32_t* indices, float* sel_scores, void* out, float* lse, void* workspace,
+                   size_t workspace_bytes, void* stream, void* const* stage_events) {
   dsa_status s = check_indexer(iargs);
   if (s != DSA_OK) return s;
-  s = check_attn(aargs, iargs->B, iargs->Lq, iargs->Lk);
+  s = kargs ? check_kv4_attn(kargs, iargs->B, iargs->Lq, iargs->Lk) : check_attn(aargs, iargs->B, iargs->Lq, iargs->Lk);
   if (s != DSA_OK) return s;
+  const int H = kargs ? kargs->H : aargs->H, d_v = kargs ? kargs->d_v : aargs->d_v;
   if (!indices || !out || !aligned16(indices) || !aligned16(out)) return DSA_ERR_INVALID_ARG;
   if (lse && !aligned16(lse)) return DSA_ERR_INVALID_ARG;
   if (sel_scores && !aligned16(sel_scores)) return DSA_ERR_INVALID_ARG;
   if (k < 1 || k > kMaxK) return DSA_ERR_UNSUPPORTED;
-  const size_t attn_need = attn_ws_bytes(iargs->B, iargs->Lq, k, aargs->H, aargs->d_v);
+  const size_t attn_need = attn_ws_bytes(iargs->B, iargs->Lq, k, H, d_v);
   if (!workspace || !aligned16(workspace)) return DSA_ERR_WORKSPACE;
   // Staged selection when the workspace holds the score matrix (the faster path),
   // else the fused indexer + top-k with its candidate lists.
@@ -729,11 +837,32 @@ dsa_status dsa_forward_timed(const dsa_indexer_args* iargs, const dsa_attn_args*
   }
   // Dense mode: the attention kernel reads keys 0..t as contiguous tiles and writes
   // the index lists itself (no top-k launch, no gathers).
-  s = run_attn(aargs, iargs->B, iargs->Lq, iargs->Lk, iargs->q_offset, true, indices, k, out, lse, attn_ws,
-               attn_ws_size, st, dense ? indices : nullptr);
+  int32_t* dense_out = dense ? indices : nullptr;
+  s = kargs ? run_attn_kv4(kargs, iargs->B, iargs->Lq, iargs->Lk, iargs->q_offset, true, indices, k, out, lse, attn_ws,
+                           attn_ws_size, st, dense_out)
+            : run_attn(aargs, iargs->B, iargs->Lq, iargs->Lk, iargs->q_offset, true, indices, k, out, lse, attn_ws,
+                       attn_ws_size, st, dense_out);
   if (s != DSA_OK) return s;
   if (!mark(3)) return DSA_ERR_CUDA;
   return DSA_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+dsa_status dsa_forward_timed(const dsa_indexer_args* iargs, const dsa_attn_args* aargs, int k, int32_t* indices,
+                             float* sel_scores, void* out, float* lse, void* workspace, size_t workspace_bytes,
+                             void* stream, void* const* stage_events) {
+  return forward(iargs, aargs, nullptr, k, indices, sel_scores, out, lse, workspace, workspace_bytes, stream,
+                 stage_events);
+}
+
+dsa_status dsa_forward_kv4(const dsa_indexer_args* iargs, const dsa_kv4_attn_args* kargs, int k, int32_t* indices,
+                           float* sel_scores, void* out, float* lse, void* workspace, size_t workspace_bytes,
+                           void* stream) {
+  if (!kargs) return DSA_ERR_INVALID_ARG;
+  return forward(iargs, nullptr, kargs, k, indices, sel_scores, out, lse, workspace, workspace_bytes, stream, nullptr);
 }
 
 dsa_status dsa_forward(const dsa_indexer_args* iargs, const dsa_attn_args* aargs, int k, int32_t* indices,

@@ -106,8 +106,15 @@ struct AttnParams {
   float* lse;             // [B, Lq, H] or null (splits == 1)
   float* part_o;          // [B*Lq, splits, H, d_v] fp32 (splits > 1)
   float* part_lse;        // [B*Lq, splits, H] fp32 (splits > 1)
+  // ---- sliding window (window > 0): row (b, i) at t = (start ? start[b] : q_offset) + i sees
+  // keys (t - window, t] and [0, sinks); no index lists
+  int window, sinks;
+  const int32_t* start;   // [B] or null
+  // ---- 4-bit cache (codes set): indices (or dense) pick its rows
+  const uint8_t* codes;   // [B, Lk, d_v / 2]
+  const __nv_bfloat16* scales;   // [B, Lk, d_v / 32]
+  const __nv_bfloat16* tail;     // [B, Lk, d_qk - d_v]
 };
-size_t attn_smem_bytes(int d_qk, int d_v);
 cudaError_t launch_sparse_attn(const AttnParams& p, int d_qk, int d_v, const CUtensorMap& tq,
                                const CUtensorMap& tkv, const CUtensorMap& tkv_tile, int grid_clusters,
                                cudaStream_t stream);

@@ -57,32 +57,55 @@ namespace {
 
 constexpr int kTileKeys = 128;       // keys per tile (pair)
 constexpr int kHalfKeys = 64;        // keys per CTA in S, and keys per V stage
-constexpr int kKStages = 6;          // K-chunk ring depth (8 KB stages)
-constexpr int kVStages = 3;          // V ring depth (64 keys x this CTA's value planes)
 constexpr int kPBufs = 2;            // P buffers (2 planes each: keys 0-63, 64-127)
 constexpr int kMaxIdx = 2048;        // selected positions per unit (staged in shared memory)
 constexpr int kMmaWarp = 4;           // TMEM owner + S issuer
 constexpr int kPvWarp = 5;            // P.V issuer
-// Loaders own ring slots, so a warp waits only on its own slots (in ring order)
-// and the stages of different slots are issued in parallel.  Key chunks: a team
-// of kKTeamWarps warps owns kKTeamSlots consecutive slots and splits each chunk's
-// 16 gathers; value stages: kVWarpsPerSlot warps per slot split its gathers.
-constexpr int kKTeamWarps = 3;
-constexpr int kKTeamSlots = 2;
-constexpr int kVWarpsPerSlot = 3;
-constexpr int kKWarp0 = 6;           // key-chunk loaders
-constexpr int kKWarps = kKStages / kKTeamSlots * kKTeamWarps;
-constexpr int kVWarp0 = kKWarp0 + kKWarps;   // value-stage loaders
-constexpr int kVWarps = kVStages * kVWarpsPerSlot;
-constexpr int kThreads = 32 * (kVWarp0 + kVWarps);   // 768
+// Where the keys come from.
+enum AttnMode {
+  kSelected = 0,   // bf16 rows picked by an index list (or, dense, rows 0..t)
+  kWindow = 1,     // bf16 rows of a sliding window and the first `sinks` positions
+  kPacked = 2      // rows of the 4-bit cache picked by an index list
+};
+// Rings, loader warps and registers of a mode.
+//
+// kSelected, kWindow: loaders own ring slots, so a warp waits only on its own slots
+// (in ring order) and the stages of different slots are issued in parallel.  Key
+// chunks: a team of kKTeamWarps warps owns kKTeamSlots consecutive slots and splits
+// each chunk's 16 gathers; value stages: kVWarpsPerSlot warps per slot split its gathers.
+// A window's rows are mostly contiguous (boxes of 16 rows instead of gathers of 4), so
+// one warp per slot issues fast enough; that leaves room for a fourth value stage
+// (it also needs no staged index lists) and for 128 registers in every thread.
+//
+// kPacked: every key (value) loader warp converts its 8 rows of every chunk, so all of
+// them pass every slot.
+//
+// Register split: a CTA of 768 threads launches with 80 registers per thread (6 warps
+// per SM sub-partition); the softmax warpgroup then takes 120 and the other
+// warpgroups (MMA issuers, loaders) keep 72.
+template <int MODE>
+struct Cfg {
+  static constexpr int kKStages = 6;                   // K-chunk ring depth (8 KB stages)
+  static constexpr int kVStages = MODE == kWindow ? 4 : 3;   // V ring depth (64 keys x this CTA's value planes)
+  static constexpr int kKTeamWarps = MODE == kWindow ? 1 : 3;
+  static constexpr int kKTeamSlots = MODE == kWindow ? 1 : 2;
+  static constexpr int kVWarpsPerSlot = MODE == kWindow ? 1 : 3;
+  static constexpr int kKWarp0 = MODE == kPacked ? 8 : 6;   // key-chunk loaders
+  static constexpr int kKWarps = MODE == kPacked ? 8 : kKStages / kKTeamSlots * kKTeamWarps;
+  static constexpr int kVWarp0 = kKWarp0 + kKWarps;    // value-stage loaders
+  static constexpr int kVWarps = MODE == kPacked ? 8 : kVStages * kVWarpsPerSlot;
+  static constexpr int kThreads = 32 * (kVWarp0 + kVWarps);   // 768 (kWindow: 512)
+  static constexpr int kStageWarps = MODE == kPacked ? 2 : kVWarps;   // warps that stage the indices
+  static constexpr int kFillers = MODE == kPacked ? 2 * kKWarps : 1;  // arrivals that fill a ring slot
+  static constexpr bool kSplitRegs = kThreads > 512;
+};
+static_assert(Cfg<kPacked>::kKWarps == 8 && Cfg<kPacked>::kVWarps == 8, "8 warps x 8 rows convert 64 keys");
+constexpr int kMaxKStages = 6, kMaxVStages = 4;
 constexpr int kStageBatch = 8;       // index words in flight per warp while staging
-// Register split: the CTA launches with 80 registers per thread (6 warps per SM
-// sub-partition); the softmax warpgroup then takes 120 and the other warpgroups
-// (MMA issuers, loaders) keep 72.
 constexpr uint32_t kRegsLaunch = 80;
 constexpr uint32_t kRegsSoftmax = 120;
 constexpr uint32_t kRegsOther = 72;
-static_assert(128 * kRegsSoftmax + (kThreads - 128) * kRegsOther <= kThreads * kRegsLaunch,
+static_assert(128 * kRegsSoftmax + (768 - 128) * kRegsOther <= 768 * kRegsLaunch,
               "register split exceeds the launch allocation");
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kPlane64 = 64 * 128;    // 64 rows x 128 B  (Q plane, K stage, V plane, P plane)
@@ -94,8 +117,8 @@ constexpr int kMaxChunks = 9;
 
 struct AttnBarriers {
   uint64_t q_full[kMaxChunks], q_empty[kMaxChunks];
-  uint64_t k_full[kKStages], k_empty[kKStages];
-  uint64_t v_full[kVStages], v_empty[kVStages];
+  uint64_t k_full[kMaxKStages], k_empty[kMaxKStages];
+  uint64_t v_full[kMaxVStages], v_empty[kMaxVStages];
   uint64_t s_full[2], s_empty[2];
   uint64_t p_full[kPBufs], p_empty[kPBufs];
   uint64_t o_full, o_empty, final_s, final_pv;
@@ -119,8 +142,10 @@ struct VShape {
 // A unit is one query row's key-tile range [j0, j1) (the whole row without split-k).
 struct Unit {
   int row, b, t, j0, j1, split;
+  int n_sinks, lo, n_valid;   // kWindow: slots 0..n_sinks-1 are keys 0.., the others keys lo..; n_valid slots
 };
 
+template <int MODE>
 __device__ __forceinline__ Unit decode_unit(const AttnParams& p, int u) {
   Unit U;
   const int n_rows = p.B * p.Lq;
@@ -129,7 +154,18 @@ __device__ __forceinline__ Unit decode_unit(const AttnParams& p, int u) {
   U.b = U.row / p.Lq;
   U.t = p.q_offset + U.row % p.Lq;
   int nt = p.n_tiles;
-  if (p.compact) {
+  if constexpr (MODE == kWindow) {
+    // Query position t sees keys max(0, t - window + 1) .. t and 0 .. sinks - 1, all
+    // below Lk; a position outside the sequence (a padded row's start) sees what of
+    // that exists, possibly nothing.
+    const long long t = (long long)(p.start ? __ldg(p.start + U.b) : p.q_offset) + U.row % p.Lq;
+    const long long lo = max(0ll, t - p.window + 1), hi = min(t, (long long)p.Lk - 1);
+    U.n_sinks = (int)min(min((long long)p.sinks, lo), (long long)p.Lk);
+    if (t < 0) U.n_sinks = 0;
+    U.lo = (int)min(lo, (long long)p.Lk);
+    U.n_valid = U.n_sinks + (int)max(0ll, hi - lo + 1);
+    nt = (U.n_valid + kTileKeys - 1) / kTileKeys;
+  } else if (p.compact) {
     const int nvalid = min(p.k, U.t + 1);
     nt = (nvalid + kTileKeys - 1) / kTileKeys;
   }
@@ -140,9 +176,10 @@ __device__ __forceinline__ Unit decode_unit(const AttnParams& p, int u) {
 
 // First unit at or after u (stepping by the cluster count) that has key tiles;
 // returns p.n_units when there is none.
+template <int MODE>
 __device__ __forceinline__ int next_unit(const AttnParams& p, int u, int step, Unit& U) {
   for (; u < p.n_units; u += step) {
-    U = decode_unit(p, u);
+    U = decode_unit<MODE>(p, u);
     if (U.j0 < U.j1) return u;
   }
   return p.n_units;
@@ -160,12 +197,242 @@ __device__ __forceinline__ int4 gather_rows4(const int32_t* rows, int pos) {
   return *reinterpret_cast<const int4*>(rows + pos);
 }
 
+// kWindow: the key at slot x of a unit.  Slots behind the last valid one repeat it: their
+// logits are masked, and a zero probability times a row that may hold anything (NaN) would
+// still reach the output.
+__device__ __forceinline__ int window_key(const Unit& U, int x) {
+  x = min(x, U.n_valid - 1);
+  return x < U.n_sinks ? x : U.lo + (x - U.n_sinks);
+}
+
+// kWindow: 64 rows (slots x0 ..) of 64 columns from column col into a plane, lanes 0-15,
+// four rows each: one box per 16 rows that are consecutive keys, else gathers of four.
+// Either way 8 KB complete on the barrier.
+__device__ __forceinline__ void window_load(const AttnParams& p, const Unit& U, int x0, uint8_t* plane,
+                                            const void* tmap_rows, const void* tmap_box, uint32_t bar, int col,
+                                            int lane) {
+  const int x = x0 + lane / 4 * 16, base = U.b * p.Lk;
+  const int first = window_key(U, x);
+  if (x >= U.n_valid && U.n_valid - U.n_sinks >= 16) {
+    // nothing valid here: any 16 valid rows will do
+    if (lane % 4 == 0) tma_load_2d_pair(plane + lane * 512, tmap_box, bar, col, base + U.lo);
+  } else if (x + 15 < U.n_valid && window_key(U, x + 15) == first + 15) {
+    if (lane % 4 == 0) tma_load_2d_pair(plane + lane * 512, tmap_box, bar, col, base + first);
+  } else {
+    const int y = x0 + lane * 4;
+    tma_gather4_pair(plane + lane * 512, tmap_rows, bar, col, base + window_key(U, y), base + window_key(U, y + 1),
+                     base + window_key(U, y + 2), base + window_key(U, y + 3));
+  }
+}
+
+// kPacked: 8 columns of the 4-bit cache as bf16.  Nibble n stands for n - 8: put at bits
+// 3-6 of bf16's 16.0 it makes 16 + n, and one fused multiply-add (16 + n) * s - 24 s gives
+// (n - 8) s exactly, since s has 5 significant bits and |n - 8| 3 (and 24 s is exact).
+__device__ __forceinline__ uint4 unpack_codes(uint32_t w, __nv_bfloat162 s, __nv_bfloat162 off) {
+  uint32_t r[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const uint32_t sh = k == 0 ? w << 3 : w >> (4 * k - 3);
+    uint32_t b = (sh & 0x00780078u) | 0x41804180u;
+    __nv_bfloat162 v = *reinterpret_cast<__nv_bfloat162*>(&b);
+    v = __hfma2(v, s, off);
+    r[k] = *reinterpret_cast<uint32_t*>(&v);
+  }
+  return make_uint4(r[0], r[1], r[2], r[3]);
+}
+
+// 16 columns (two words) of row `r8` of an 8-row swizzle atom, from 16-byte column 2 * part.
+__device__ __forceinline__ void store_codes(uint8_t* atom, int r8, int part, uint32_t w0, uint32_t w1,
+                                            uint32_t scale_bits) {
+  const uint32_t dup = scale_bits | (scale_bits << 16);
+  const __nv_bfloat162 s = *reinterpret_cast<const __nv_bfloat162*>(&dup);
+  const __nv_bfloat162 off = __hmul2(s, __floats2bfloat162_rn(-24.f, -24.f));
+  uint8_t* row = atom + r8 * 128;
+  *reinterpret_cast<uint4*>(row + (((2 * part) ^ r8) * 16)) = unpack_codes(w0, s, off);
+  *reinterpret_cast<uint4*>(row + (((2 * part + 1) ^ r8) * 16)) = unpack_codes(w1, s, off);
+}
+
+// kPacked loaders walk the tiles of all their units one after the other; the loads of a
+// tile are issued while the tile before it is converted, across unit boundaries too.
+struct TileCursor {
+  Unit U;
+  int u, j;               // unit (>= n_units: past the end) and tile
+  uint32_t ucount;        // units entered so far
+};
+
+// Cache rows of this lane's slots in the cursor's tile: slot `x0` (and x0 + 64 when TWO),
+// -1 for a masked one.  Waits for the unit's staged indices on entering it and releases
+// them with its last tile.
+template <bool TWO>
+__device__ __forceinline__ bool cursor_rows(AttnBarriers& S, const int32_t* idx_sm, const TileCursor& c, int x0,
+                                            int& r0, int& r1, volatile uint32_t* abort_flag) {
+  const uint32_t ib = (c.ucount - 1) & 1u, uph = ((c.ucount - 1) >> 1) & 1u;
+  if (c.j == c.U.j0 && !mbar_wait_warp(&S.idx_full[ib], uph, abort_flag)) return false;
+  const int32_t* idx = idx_sm + ib * kMaxIdx + (c.j - c.U.j0) * kTileKeys + x0;
+  r0 = idx[0];
+  if (TWO) r1 = idx[kHalfKeys];
+  if (c.j == c.U.j1 - 1) {
+    __syncwarp();
+    if (lane_id() == 0) mbar_arrive(&S.idx_empty[ib]);
+  }
+  return true;
+}
+
+__device__ __forceinline__ void cursor_next(const AttnParams& p, TileCursor& c, int n_clusters) {
+  if (++c.j < c.U.j1) return;
+  c.u = next_unit<kPacked>(p, c.u + n_clusters, n_clusters, c.U);
+  c.j = c.U.j0;
+  ++c.ucount;
+}
+
+// Key loaders of kPacked: warp `pw` converts rows 8 pw .. 8 pw + 7 of this CTA's 64 keys,
+// four lanes to a row, 16 columns of every 64-column chunk to a lane.
 template <int NC, int DV>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+__device__ __forceinline__ void packed_keys(const AttnParams& p, AttnBarriers& S, uint8_t* k_sm,
+                                            const int32_t* idx_sm, int pw, uint32_t rank, int cluster_id,
+                                            int n_clusters, volatile uint32_t* abort_flag) {
+  constexpr int kKStages = Cfg<kPacked>::kKStages;
+  constexpr int kLat = DV / 64;                        // chunks of 4-bit columns; then one bf16 tail chunk
+  static_assert(NC == kLat + 1, "one tail chunk");
+  const int lane = (int)lane_id(), r8 = lane / 4, part = lane % 4;
+  TileCursor c;
+  c.u = next_unit<kPacked>(p, cluster_id, n_clusters, c.U);
+  if (c.u >= p.n_units) return;
+  c.j = c.U.j0;
+  c.ucount = 1;
+  const int x0 = (int)rank * kHalfKeys + pw * 8 + r8;
+  int row, unused;
+  if (!cursor_rows<false>(S, idx_sm, c, x0, row, unused, abort_flag)) return;
+  uint32_t code[kLat * 2], sc[kLat / 2];
+  uint4 tail[2];
+  // A masked row gets scale 0 and an all-zero tail: keys of zeros, no load.
+  auto load_code = [&](int q, int r) {                 // 16 bytes: chunks 2q, 2q + 1
+    uint4 v = make_uint4(0, 0, 0, 0);
+    if (r >= 0) v = __ldg(reinterpret_cast<const uint4*>(p.codes + (size_t)r * (DV / 2) + part * (DV / 8)) + q);
+    code[4 * q] = v.x; code[4 * q + 1] = v.y; code[4 * q + 2] = v.z; code[4 * q + 3] = v.w;
+  };
+  auto load_rest = [&](int r) {
+    const uint8_t* ss = reinterpret_cast<const uint8_t*>(p.scales) + (size_t)max(r, 0) * (DV / 16) + (part / 2) * (DV / 32);
+    if constexpr (kLat == 8) {
+      uint4 v = make_uint4(0, 0, 0, 0);
+      if (r >= 0) v = __ldg(reinterpret_cast<const uint4*>(ss));
+      sc[0] = v.x; sc[1] = v.y; sc[2] = v.z; sc[3] = v.w;
+    } else {
+      sc[0] = r >= 0 ? __ldg(reinterpret_cast<const uint32_t*>(ss)) : 0u;
+    }
+    const uint4* ts = reinterpret_cast<const uint4*>(p.tail + (size_t)max(r, 0) * 64) + part * 2;
+    tail[0] = tail[1] = make_uint4(0, 0, 0, 0);
+    if (r >= 0) { tail[0] = __ldg(ts); tail[1] = __ldg(ts + 1); }
+  };
+#pragma unroll
+  for (int q = 0; q < kLat / 2; ++q) load_code(q, row);
+  load_rest(row);
+  uint32_t kc = 0;
+  while (c.u < p.n_units) {
+    cursor_next(p, c, n_clusters);
+    int next = -1;
+    const bool more = c.u < p.n_units;
+    if (more && !cursor_rows<false>(S, idx_sm, c, x0, next, unused, abort_flag)) return;
+#pragma unroll
+    for (int ch = 0; ch < NC; ++ch, ++kc) {
+      const uint32_t st = kc % kKStages;
+      if (!mbar_wait_warp(&S.k_empty[st], ((kc / kKStages) & 1u) ^ 1u, abort_flag)) return;
+      uint8_t* atom = k_sm + st * kPlane64 + pw * 1024;
+      if (ch < kLat) {
+        const uint32_t sw = sc[ch / 2];
+        store_codes(atom, r8, part, code[2 * ch], code[2 * ch + 1], ch % 2 ? sw >> 16 : sw & 0xffffu);
+        if (ch % 2 == 1) load_code(ch / 2, next);
+      } else {
+        *reinterpret_cast<uint4*>(atom + r8 * 128 + (((2 * part) ^ r8) * 16)) = tail[0];
+        *reinterpret_cast<uint4*>(atom + r8 * 128 + (((2 * part + 1) ^ r8) * 16)) = tail[1];
+        load_rest(next);
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_remote(mapa_shared(smem_u32(&S.k_full[st]), 0));
+    }
+    if (!more) break;
+  }
+}
+
+// Value loaders of kPacked: warp `pw` converts rows 8 pw .. of both 64-key halves of the
+// tile, this CTA's value columns.
+template <int DV>
+__device__ __forceinline__ void packed_values(const AttnParams& p, AttnBarriers& S, uint8_t* v_sm,
+                                              const int32_t* idx_sm, int pw, uint32_t rank, int cluster_id,
+                                              int n_clusters, volatile uint32_t* abort_flag) {
+  using VS = VShape<DV>;
+  constexpr int kVStages = Cfg<kPacked>::kVStages;
+  constexpr int kPl = VS::kPlanes;                     // 64-column planes of a stage
+  constexpr int kSt = 2 * VS::kNpv;                    // stages per tile: key half, value block
+  const int lane = (int)lane_id(), r8 = lane / 4, part = lane % 4;
+  TileCursor c;
+  c.u = next_unit<kPacked>(p, cluster_id, n_clusters, c.U);
+  if (c.u >= p.n_units) return;
+  c.j = c.U.j0;
+  c.ucount = 1;
+  const int x0 = pw * 8 + r8;
+  int row[2];
+  if (!cursor_rows<true>(S, idx_sm, c, x0, row[0], row[1], abort_flag)) return;
+  uint32_t code[kSt][2 * kPl], sc[kSt];
+  auto load = [&](int s, int r) {
+    // chunk of the stage's first plane: value block s % kNpv, this CTA's half of it
+    const int ch = (s % VS::kNpv) * (VS::kN / 64) + (int)rank * kPl;
+    const uint8_t* cs = p.codes + (size_t)max(r, 0) * (DV / 2) + part * (DV / 8) + ch * 8;
+    const __nv_bfloat16* ss = p.scales + (size_t)max(r, 0) * (DV / 32) + (part / 2) * (DV / 64) + ch;
+    if constexpr (kPl == 2) {
+      uint4 v = make_uint4(0, 0, 0, 0);
+      sc[s] = 0;
+      if (r >= 0) {
+        v = __ldg(reinterpret_cast<const uint4*>(cs));
+        sc[s] = __ldg(reinterpret_cast<const uint32_t*>(ss));
+      }
+      code[s][0] = v.x; code[s][1] = v.y; code[s][2] = v.z; code[s][3] = v.w;
+    } else {
+      uint2 v = make_uint2(0, 0);
+      sc[s] = 0;
+      if (r >= 0) {
+        v = __ldg(reinterpret_cast<const uint2*>(cs));
+        sc[s] = __ldg(reinterpret_cast<const unsigned short*>(ss));
+      }
+      code[s][0] = v.x; code[s][1] = v.y;
+    }
+  };
+#pragma unroll
+  for (int s = 0; s < kSt; ++s) load(s, row[s / VS::kNpv]);
+  uint32_t vc = 0;
+  while (c.u < p.n_units) {
+    cursor_next(p, c, n_clusters);
+    int next[2] = {-1, -1};
+    const bool more = c.u < p.n_units;
+    if (more && !cursor_rows<true>(S, idx_sm, c, x0, next[0], next[1], abort_flag)) return;
+#pragma unroll
+    for (int s = 0; s < kSt; ++s, ++vc) {
+      const uint32_t st = vc % kVStages;
+      if (!mbar_wait_warp(&S.v_empty[st], ((vc / kVStages) & 1u) ^ 1u, abort_flag)) return;
+#pragma unroll
+      for (int pl = 0; pl < kPl; ++pl)
+        store_codes(v_sm + st * VS::kStageBytes + pl * kPlane64 + pw * 1024, r8, part, code[s][2 * pl],
+                    code[s][2 * pl + 1], pl ? sc[s] >> 16 : sc[s] & 0xffffu);
+      load(s, next[s / VS::kNpv]);
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_remote(mapa_shared(smem_u32(&S.v_full[st]), 0));
+    }
+    if (!more) break;
+  }
+}
+
+template <int NC, int DV, int MODE>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<MODE>::kThreads, 1)
 sparse_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ CUtensorMap tmap_kv,
                    const __grid_constant__ CUtensorMap tmap_kv_tile, const AttnParams p) {
   using VS = VShape<DV>;
+  using C = Cfg<MODE>;
   static_assert(NC <= kMaxChunks, "d_qk");
+  constexpr int kKStages = C::kKStages, kVStages = C::kVStages, kKWarp0 = C::kKWarp0, kKWarps = C::kKWarps;
+  constexpr int kVWarp0 = C::kVWarp0, kVWarps = C::kVWarps, kKTeamWarps = C::kKTeamWarps;
+  constexpr int kKTeamSlots = C::kKTeamSlots, kVWarpsPerSlot = C::kVWarpsPerSlot, kStageWarps = C::kStageWarps;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   AttnBarriers& S = *reinterpret_cast<AttnBarriers*>(smem_raw);
   // 1024-byte aligned operand area (the 128-byte swizzle is address based).
@@ -188,8 +455,8 @@ sparse_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < kMaxChunks; ++i) { mbar_init(&S.q_full[i], 1); mbar_init(&S.q_empty[i], 1); }
-    for (int i = 0; i < kKStages; ++i) { mbar_init(&S.k_full[i], 1); mbar_init(&S.k_empty[i], 1); }
-    for (int i = 0; i < kVStages; ++i) { mbar_init(&S.v_full[i], 1); mbar_init(&S.v_empty[i], 1); }
+    for (int i = 0; i < kKStages; ++i) { mbar_init(&S.k_full[i], C::kFillers); mbar_init(&S.k_empty[i], 1); }
+    for (int i = 0; i < kVStages; ++i) { mbar_init(&S.v_full[i], C::kFillers); mbar_init(&S.v_empty[i], 1); }
     for (int i = 0; i < kPBufs; ++i) {
       mbar_init(&S.p_full[i], 8);      // 4 softmax warps x 2 CTAs
       mbar_init(&S.p_empty[i], 1);
@@ -197,7 +464,7 @@ sparse_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
     for (int i = 0; i < 2; ++i) {
       mbar_init(&S.s_full[i], 1);
       mbar_init(&S.s_empty[i], 8);     // 4 softmax warps x 2 CTAs
-      mbar_init(&S.idx_full[i], kVWarps);   // the value loaders stage the indices
+      mbar_init(&S.idx_full[i], kStageWarps);
       mbar_init(&S.idx_empty[i], 4 + kKWarps + kVWarps);   // softmax warps + loader warps
     }
     mbar_init(&S.o_full, 1);
@@ -222,14 +489,118 @@ sparse_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
   griddep_launch_dependents();
   griddep_wait();                                      // the previous kernel's writes are visible
 
+  // Index staging (one warp of kStageWarps, number pw): each unit's selected positions
+  // [j0*128, j1*128) go into buffer (unit ordinal % 2), one unit ahead, as the kv row to
+  // load -- batch offset applied; padding and out-of-range entries gather row b*Lk
+  // (kPacked: -1, nothing is loaded) and are masked -- plus one validity ballot per 32
+  // positions for the softmax.  Warp pw stages the 32-position words pw, pw + kStageWarps,
+  // ...  A buffer is free again once the loaders and the softmax warps are done with
+  // the unit two back.
+  auto stage = [&](const Unit& V, uint32_t buf, int pw) {
+    int32_t* dst = idx_sm + buf * kMaxIdx;
+    uint32_t* vmask = S.valid_mask[buf];
+    const int x_begin = V.j0 * kTileKeys, nwords = (V.j1 - V.j0) * (kTileKeys / 32);
+    if (p.dense) {
+      // Row t selects every position 0..t (in slot order); the bf16 loads need no
+      // staged rows, only the validity words.  The leader also writes the
+      // row's index list, and the first split its tail of -1 slots.
+      int32_t* io = p.idx_out + (size_t)V.row * p.k;
+      for (int w = pw; w < nwords; w += kStageWarps) {
+        const int x = x_begin + w * 32 + (int)lane;
+        const bool valid = x <= V.t && x < p.k;
+        const uint32_t bal = __ballot_sync(0xffffffffu, valid);
+        if (lane == 0) vmask[w] = bal;
+        if (MODE == kPacked) dst[w * 32 + (int)lane] = valid ? V.b * p.Lk + x : -1;
+        if (leader && x < p.k) io[x] = valid ? x : -1;
+      }
+      if (leader && V.split == 0) {
+        const int nt_row = (min(p.k, V.t + 1) + kTileKeys - 1) / kTileKeys;
+        for (int x = nt_row * kTileKeys + pw * 32 + (int)lane; x < p.k; x += kStageWarps * 32) io[x] = -1;
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&S.idx_full[buf]);
+      return;
+    }
+    const int32_t* src = p.indices + (size_t)V.row * p.k;
+    for (int w0 = pw; w0 < nwords; w0 += kStageWarps * kStageBatch) {
+      int sidx[kStageBatch];
+#pragma unroll
+      for (int e = 0; e < kStageBatch; ++e) {
+        const int w = w0 + e * kStageWarps, x = x_begin + w * 32 + (int)lane;
+        sidx[e] = (w < nwords && x < p.k) ? __ldg(src + x) : -1;
+      }
+#pragma unroll
+      for (int e = 0; e < kStageBatch; ++e) {
+        const int w = w0 + e * kStageWarps;
+        if (w >= nwords) break;                       // warp-uniform
+        const bool valid = (sidx[e] >= 0) && (sidx[e] < p.Lk);
+        if (MODE == kPacked) dst[w * 32 + (int)lane] = valid ? V.b * p.Lk + sidx[e] : -1;
+        else dst[w * 32 + (int)lane] = V.b * p.Lk + (valid ? sidx[e] : 0);   // validity: the ballot below
+        const uint32_t bal = __ballot_sync(0xffffffffu, valid);
+        if (lane == 0) vmask[w] = bal;
+      }
+    }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&S.idx_full[buf]);
+  };
+
   if (warp >= 4) {
-    regs_decrease<kRegsOther>();
-    if (warp >= kKWarp0 && warp < kVWarp0) {
+    if constexpr (C::kSplitRegs) regs_decrease<kRegsOther>();
+    if (MODE == kPacked && warp >= kKWarp0) {
+      // ------------------------------------------------------------------ converting loaders
+      if constexpr (MODE == kPacked) {
+        if (warp < kVWarp0)
+          packed_keys<NC, DV>(p, S, k_sm, idx_sm, (int)warp - kKWarp0, rank, cluster_id, n_clusters, abort_flag);
+        else
+          packed_values<DV>(p, S, v_sm, idx_sm, (int)warp - kVWarp0, rank, cluster_id, n_clusters, abort_flag);
+      }
+    } else if (MODE == kPacked && warp > kPvWarp) {
+      // ------------------------------------------------------------------ Q planes and index staging
+      if constexpr (MODE == kPacked) {
+        const int pw = (int)warp - (kPvWarp + 1);
+        uint32_t ucount = 0;
+        bool ok = true;
+        if (pw == 0 && lane == 0) prefetch_tmap(&tmap_q);
+        auto load_q = [&](const Unit& V) {               // planes pw, pw + kStageWarps, ...
+          if (lane == 0) {
+            const int qrow = V.row * p.H + (int)rank * 64;
+            for (int c = pw; c < NC && ok; c += kStageWarps) {
+              ok = mbar_wait(&S.q_empty[c], (ucount & 1u) ^ 1u, abort_flag);
+              if (!ok) break;
+              if (leader) mbar_arrive_expect_tx(&S.q_full[c], 2u * kPlane64);
+              tma_load_2d_pair(q_sm + c * kPlane64, &tmap_q, mapa_shared(smem_u32(&S.q_full[c]), 0), c * 64, qrow);
+            }
+          }
+          ok = __shfl_sync(0xffffffffu, ok, 0);
+        };
+        Unit U, Un;
+        int u = next_unit<MODE>(p, cluster_id, n_clusters, U);
+        if (u < p.n_units) {
+          load_q(U);
+          stage(U, 0, pw);
+        }
+        while (u < p.n_units && ok) {
+          const int un = next_unit<MODE>(p, u + n_clusters, n_clusters, Un);
+          if (ucount > 0) load_q(U);
+          if (!ok) break;
+          if (un < p.n_units) {
+            const uint32_t nb = (ucount + 1) & 1u, nph = ((ucount + 1) >> 1) & 1u;
+            ok = mbar_wait_warp(&S.idx_empty[nb], nph ^ 1u, abort_flag);
+            if (!ok) break;
+            stage(Un, nb, pw);
+          }
+          ++ucount;
+          u = un;
+          U = Un;
+        }
+      }
+    } else if (warp >= kKWarp0 && warp < kVWarp0) {
       // ------------------------------------------------------------------ key loaders
       // Per unit: the Q planes (plane c from warp c % kKWarps), then for each tile
       // its NC key chunks (this CTA's 64 keys x 64 columns).  Chunk kc goes to
       // ring slot kc % kKStages; the team that owns that slot issues its 16
       // four-row gathers, groups g = part, part + kKTeamWarps, ...
+      if constexpr (MODE != kPacked) {
       const int pw = (int)warp - kKWarp0;
       const uint32_t my_team = (uint32_t)(pw / kKTeamWarps);
       const int part = pw % kKTeamWarps;
@@ -237,11 +608,11 @@ sparse_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
       bool ok = true;
       if (pw == 0 && lane == 0) {
         prefetch_tmap(&tmap_q);
-        prefetch_tmap(p.dense ? &tmap_kv_tile : &tmap_kv);
+        prefetch_tmap(MODE == kWindow || p.dense ? &tmap_kv_tile : &tmap_kv);
       }
       Unit U;
-      for (int u = next_unit(p, cluster_id, n_clusters, U); u < p.n_units && ok;
-           u = next_unit(p, u + n_clusters, n_clusters, U)) {
+      for (int u = next_unit<MODE>(p, cluster_id, n_clusters, U); u < p.n_units && ok;
+           u = next_unit<MODE>(p, u + n_clusters, n_clusters, U)) {
         const uint32_t ib = ucount & 1u, uph = (ucount >> 1) & 1u;
         if (lane == 0) {
           const int qrow = U.row * p.H + (int)rank * 64;
@@ -254,7 +625,7 @@ sparse_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
         }
         ok = __shfl_sync(0xffffffffu, ok, 0);
         if (!ok) break;
-        ok = mbar_wait_warp(&S.idx_full[ib], uph, abort_flag);
+        if (MODE != kWindow) ok = mbar_wait_warp(&S.idx_full[ib], uph, abort_flag);
         if (!ok) break;
         const int32_t* idx = idx_sm + ib * kMaxIdx;
         // The unit's chunks are kc_u .. kc_u + nk - 1; chunk x goes to slot x % kKStages.
@@ -274,7 +645,7 @@ sparse_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
           // have nothing to load and must not wait either (a waiter that adds
           // nothing to a phase can fall two phases behind, where its parity test
           // would no longer see the phase it waits for).
-          if (p.dense && part != 0) continue;
+          if (MODE == kSelected && p.dense && part != 0) continue;
           bool w_ok = true;
           if (lane == 0) {
             w_ok = mbar_wait(&S.k_empty[st], ph ^ 1u, abort_flag);
@@ -282,6 +653,12 @@ sparse_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
           }
           if (!__shfl_sync(0xffffffffu, w_ok, 0)) { ok = false; break; }
           const uint32_t full_l = mapa_shared(smem_u32(&S.k_full[st]), 0);
+          if constexpr (MODE == kWindow) {
+            if (lane < 16)
+              window_load(p, U, j * kTileKeys + (int)rank * kHalfKeys, k_sm + st * kPlane64, &tmap_kv, &tmap_kv_tile,
+                          full_l, c * 64, (int)lane);
+            continue;
+          }
           if (p.dense) {
             // keys 0..t are contiguous: this CTA's 64 rows of the tile in one box
             if (part == 0 && lane == 0)
@@ -297,84 +674,37 @@ sparse_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
         }
         kc = kc_u + nk;
         __syncwarp();
-        if (lane == 0) mbar_arrive(&S.idx_empty[ib]);
+        if (MODE != kWindow && lane == 0) mbar_arrive(&S.idx_empty[ib]);
         ++ucount;
+      }
       }
     } else if (warp >= kVWarp0) {
       // ------------------------------------------------------------------ value loaders
-      // Index staging: the value loaders also stage each unit's selected positions
-      // [j0*128, j1*128) into buffer (unit ordinal % 2), one unit ahead, as the kv
-      // row to gather -- batch offset applied; padding and out-of-range entries
-      // gather row b*Lk and are masked -- plus one validity ballot per 32
-      // positions for the softmax.  Warp pw stages the
-      // 32-position words pw, pw + kVWarps, ...  A buffer is free again once the
-      // loaders and the softmax warps are done with the unit two back.
+      // The value loaders also stage the indices, one unit ahead.
       // Value stages: per tile, 2 x kNpv stages of 64 keys (kh) x this CTA's kN/2
       // columns of value block h, i.e. all 128 keys of the tile across the two halves.
+      if constexpr (MODE != kPacked) {
       const int pw = (int)warp - kVWarp0;
       const uint32_t my_slot = (uint32_t)(pw / kVWarpsPerSlot);
       const int part = pw % kVWarpsPerSlot;
       uint32_t ucount = 0, vc = 0;
       bool ok = true;
-      auto stage = [&](const Unit& V, uint32_t buf) {
-        int32_t* dst = idx_sm + buf * kMaxIdx;
-        uint32_t* vmask = S.valid_mask[buf];
-        const int x_begin = V.j0 * kTileKeys, nwords = (V.j1 - V.j0) * (kTileKeys / 32);
-        if (p.dense) {
-          // Row t selects every position 0..t (in slot order); the loads need no
-          // staged rows, only the validity words.  The leader also writes the
-          // row's index list, and the first split its tail of -1 slots.
-          int32_t* io = p.idx_out + (size_t)V.row * p.k;
-          for (int w = pw; w < nwords; w += kVWarps) {
-            const int x = x_begin + w * 32 + (int)lane;
-            const bool valid = x <= V.t && x < p.k;
-            const uint32_t bal = __ballot_sync(0xffffffffu, valid);
-            if (lane == 0) vmask[w] = bal;
-            if (leader && x < p.k) io[x] = valid ? x : -1;
-          }
-          if (leader && V.split == 0) {
-            const int nt_row = (min(p.k, V.t + 1) + kTileKeys - 1) / kTileKeys;
-            for (int x = nt_row * kTileKeys + pw * 32 + (int)lane; x < p.k; x += kVWarps * 32) io[x] = -1;
-          }
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&S.idx_full[buf]);
-          return;
-        }
-        const int32_t* src = p.indices + (size_t)V.row * p.k;
-        for (int w0 = pw; w0 < nwords; w0 += kVWarps * kStageBatch) {
-          int sidx[kStageBatch];
-#pragma unroll
-          for (int e = 0; e < kStageBatch; ++e) {
-            const int w = w0 + e * kVWarps, x = x_begin + w * 32 + (int)lane;
-            sidx[e] = (w < nwords && x < p.k) ? __ldg(src + x) : -1;
-          }
-#pragma unroll
-          for (int e = 0; e < kStageBatch; ++e) {
-            const int w = w0 + e * kVWarps;
-            if (w >= nwords) break;                       // warp-uniform
-            const bool valid = (sidx[e] >= 0) && (sidx[e] < p.Lk);
-            dst[w * 32 + (int)lane] = V.b * p.Lk + (valid ? sidx[e] : 0);   // validity: the ballot below
-            const uint32_t bal = __ballot_sync(0xffffffffu, valid);
-            if (lane == 0) vmask[w] = bal;
-          }
-        }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&S.idx_full[buf]);
-      };
       Unit U, Un;
-      int u = next_unit(p, cluster_id, n_clusters, U);
-      if (u < p.n_units) stage(U, 0);                    // buffer 0 starts free
+      int u = next_unit<MODE>(p, cluster_id, n_clusters, U);
+      if (MODE != kWindow && u < p.n_units) stage(U, 0, pw);   // buffer 0 starts free
       while (u < p.n_units && ok) {
         const uint32_t ib = ucount & 1u, uph = (ucount >> 1) & 1u;
-        const int un = next_unit(p, u + n_clusters, n_clusters, Un);
-        if (un < p.n_units) {
-          const uint32_t nb = (ucount + 1) & 1u, nph = ((ucount + 1) >> 1) & 1u;
-          ok = mbar_wait_warp(&S.idx_empty[nb], nph ^ 1u, abort_flag);
+        const int un = next_unit<MODE>(p, u + n_clusters, n_clusters, Un);
+        if (MODE != kWindow) {
+          if (un < p.n_units) {
+            const uint32_t nb = (ucount + 1) & 1u, nph = ((ucount + 1) >> 1) & 1u;
+            ok = mbar_wait_warp(&S.idx_empty[nb], nph ^ 1u, abort_flag);
+            if (!ok) break;
+            stage(Un, nb, pw);
+          }
+          ok = mbar_wait_warp(&S.idx_full[ib], uph, abort_flag);
           if (!ok) break;
-          stage(Un, nb);
         }
-        ok = mbar_wait_warp(&S.idx_full[ib], uph, abort_flag);
-        if (!ok) break;
         const int32_t* idx = idx_sm + ib * kMaxIdx;
         // The unit's value stages are vc_u .. vc_u + nv - 1 (per tile: key half kh,
         // then value block h); stage x goes to slot x % kVStages, and this warp visits
@@ -386,7 +716,7 @@ sparse_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
           const uint32_t st = my_slot, ph = (x / kVStages) & 1u;
           const uint32_t rem = (x - vc_u) % kPerTile;
           const int j = U.j0 + (int)((x - vc_u) / kPerTile), kh = (int)(rem / VS::kNpv), h = (int)(rem % VS::kNpv);
-          if (p.dense && part != 0) continue;         // one issuing warp per slot (see the key loaders)
+          if (MODE == kSelected && p.dense && part != 0) continue;   // one issuing warp per slot (see the key loaders)
           bool w_ok = true;
           if (lane == 0) {
             w_ok = mbar_wait(&S.v_empty[st], ph ^ 1u, abort_flag);
@@ -394,6 +724,13 @@ sparse_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
           }
           if (!__shfl_sync(0xffffffffu, w_ok, 0)) { ok = false; break; }
           const uint32_t full_l = mapa_shared(smem_u32(&S.v_full[st]), 0);
+          if constexpr (MODE == kWindow) {
+            const int pl = (int)lane / 16;
+            if (pl < VS::kPlanes)
+              window_load(p, U, j * kTileKeys + kh * kHalfKeys, v_sm + st * VS::kStageBytes + pl * kPlane64, &tmap_kv,
+                          &tmap_kv_tile, full_l, h * VS::kN + (int)rank * (VS::kN / 2) + pl * 64, (int)lane % 16);
+            continue;
+          }
           if (p.dense) {
             // 64 contiguous keys x this CTA's value columns: one box per plane
             if (part == 0 && lane < (uint32_t)VS::kPlanes) {
@@ -414,10 +751,11 @@ sparse_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
         }
         vc = vc_u + nv;
         __syncwarp();
-        if (lane == 0) mbar_arrive(&S.idx_empty[ib]);
+        if (MODE != kWindow && lane == 0) mbar_arrive(&S.idx_empty[ib]);
         ++ucount;
         u = un;
         U = Un;
+      }
       }
     } else if (warp == kMmaWarp) {
       // ------------------------------------------------------------------ S issuer
@@ -431,8 +769,8 @@ sparse_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
         uint32_t ucount = 0, kc = 0, sc = 0;
         bool ok = true;
         Unit U;
-        for (int u = next_unit(p, cluster_id, n_clusters, U); u < p.n_units && ok;
-             u = next_unit(p, u + n_clusters, n_clusters, U)) {
+        for (int u = next_unit<MODE>(p, cluster_id, n_clusters, U); u < p.n_units && ok;
+             u = next_unit<MODE>(p, u + n_clusters, n_clusters, U)) {
           for (int j = U.j0; j < U.j1 && ok; ++j) {
             const uint32_t sb = sc & 1u;
             ok = mbar_wait(&S.s_empty[sb], ((sc >> 1) & 1u) ^ 1u, abort_flag, true);
@@ -442,7 +780,7 @@ sparse_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
             for (int c = 0; c < NC; ++c) {
               if (j == U.j0 && !mbar_wait(&S.q_full[c], ucount & 1u, abort_flag)) { ok = false; break; }
               const uint32_t st = kc % kKStages, ph = (kc / kKStages) & 1u;
-              if (!mbar_wait(&S.k_full[st], ph, abort_flag)) { ok = false; break; }
+              if (!mbar_wait(&S.k_full[st], ph, abort_flag, MODE == kPacked)) { ok = false; break; }
               tc_fence_after();
               // descriptor start addresses advance 32 B (encoded 2) per K step of 16
               const uint64_t ad = q_desc + (uint64_t)(c * (kPlane64 >> 4));
@@ -476,8 +814,8 @@ sparse_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
         uint32_t vc = 0, pc = 0, oc = 0;
         bool ok = true;
         Unit U;
-        for (int u = next_unit(p, cluster_id, n_clusters, U); u < p.n_units && ok;
-             u = next_unit(p, u + n_clusters, n_clusters, U)) {
+        for (int u = next_unit<MODE>(p, cluster_id, n_clusters, U); u < p.n_units && ok;
+             u = next_unit<MODE>(p, u + n_clusters, n_clusters, U)) {
           for (int j = U.j0; j < U.j1 && ok; ++j) {
             const bool first = (j == U.j0);
             ok = mbar_wait(&S.p_full[pc & 1u], (pc >> 1) & 1u, abort_flag, true);
@@ -487,7 +825,7 @@ sparse_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
             for (int kh = 0; kh < 2 && ok; ++kh) {
               for (int h = 0; h < VS::kNpv; ++h) {
                 const uint32_t st = vc % kVStages, ph = (vc / kVStages) & 1u;
-                if (!mbar_wait(&S.v_full[st], ph, abort_flag)) { ok = false; break; }
+                if (!mbar_wait(&S.v_full[st], ph, abort_flag, MODE == kPacked)) { ok = false; break; }
                 tc_fence_after();
                 const uint32_t d = tmem_base + kTmemO + h * (VS::kN / 2);
                 // P advances 32 B (encoded 2) and V 16 keys = 2048 B (encoded 128) per K step
@@ -512,7 +850,7 @@ sparse_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
       }
     }
   } else {
-    regs_increase<kRegsSoftmax>();
+    if constexpr (C::kSplitRegs) regs_increase<kRegsSoftmax>();
     // ------------------------------------------------------------------ softmax / epilogue
     const uint32_t l = warp * 32 + lane;          // TMEM lane = (key half, head)
     const uint32_t h = l & 63u;                   // head within this CTA
@@ -522,7 +860,7 @@ sparse_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
     uint32_t ucount = 0, sc = 0, pc = 0, oc = 0, xph = 0;
     bool ok = true;
     for (int u = cluster_id; u < p.n_units && ok; u += n_clusters) {
-      const Unit U = decode_unit(p, u);
+      const Unit U = decode_unit<MODE>(p, u);
       if (U.j0 >= U.j1) {
         // An empty split: no keys.  Partial result is (O = 0, lse = -inf).
         if (p.splits > 1 && half == 0 && head < p.H) {
@@ -531,10 +869,17 @@ sparse_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
           float4* o4 = reinterpret_cast<float4*>(p.part_o + prow * DV);
           for (int x = 0; x < DV / 4; ++x) o4[x] = make_float4(0.f, 0.f, 0.f, 0.f);
         }
+        // A window row that sees nothing.
+        if (MODE == kWindow && p.splits == 1 && half == 0 && head < p.H) {
+          const size_t orow = (size_t)U.row * p.H + head;
+          if (p.lse) p.lse[orow] = -INFINITY;
+          uint4* o4 = reinterpret_cast<uint4*>(p.out + orow * DV);
+          for (int x = 0; x < DV / 8; ++x) o4[x] = make_uint4(0u, 0u, 0u, 0u);
+        }
         continue;
       }
       const uint32_t ib = ucount & 1u, uph = (ucount >> 1) & 1u;
-      ok = mbar_wait_warp(&S.idx_full[ib], uph, abort_flag);
+      if (MODE != kWindow) ok = mbar_wait_warp(&S.idx_full[ib], uph, abort_flag);
       if (!ok) break;
       float m = -INFINITY, lsum = 0.f;
       for (int j = U.j0; j < U.j1 && ok; ++j) {
@@ -545,8 +890,16 @@ sparse_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
         // This lane's 64 logits, read from TMEM once.  Invalid entries (padding,
         // out-of-range) become -inf; whole groups are valid except in a row's last tile.
         const uint32_t s_addr = tmem_base + lane_addr + kTmemS + sb * kHalfKeys;
-        const uint32_t* vm = &S.valid_mask[ib][((j - U.j0) * kTileKeys + (int)half * kHalfKeys) / 32];
-        const uint32_t vmask0 = vm[0], vmask1 = vm[1];   // warp-uniform
+        uint32_t vmask0, vmask1;                      // warp-uniform
+        if constexpr (MODE == kWindow) {
+          const int n = U.n_valid - (j * kTileKeys + (int)half * kHalfKeys);
+          vmask0 = n >= 32 ? 0xffffffffu : n <= 0 ? 0u : (1u << n) - 1u;
+          vmask1 = n >= 64 ? 0xffffffffu : n <= 32 ? 0u : (1u << (n - 32)) - 1u;
+        } else {
+          const uint32_t* vm = &S.valid_mask[ib][((j - U.j0) * kTileKeys + (int)half * kHalfKeys) / 32];
+          vmask0 = vm[0];
+          vmask1 = vm[1];
+        }
         uint32_t v[64];
         tmem_ld32(s_addr, *reinterpret_cast<uint32_t(*)[32]>(&v[0]));
         tmem_ld32(s_addr + 32, *reinterpret_cast<uint32_t(*)[32]>(&v[32]));
@@ -627,7 +980,7 @@ sparse_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
       }
       if (!ok) break;
       __syncwarp();
-      if (lane == 0) mbar_arrive(&S.idx_empty[ib]);
+      if (MODE != kWindow && lane == 0) mbar_arrive(&S.idx_empty[ib]);
       ++ucount;
       // ---- epilogue of the unit
       ok = mbar_wait_warp(&S.o_full, oc & 1u, abort_flag);
@@ -728,11 +1081,18 @@ __global__ void __launch_bounds__(128) attn_combine_kernel(const AttnParams p) {
   if (lane == 0 && p.lse) p.lse[(size_t)row * p.H + head] = (wsum > 0.f) ? mx + logf(wsum) : -INFINITY;
 }
 
-template <int NC, int DV>
+template <int NC, int DV, int MODE>
 cudaError_t launch_t(const AttnParams& p, const CUtensorMap& tq, const CUtensorMap& tkv,
                      const CUtensorMap& tkv_tile, int grid_clusters, cudaStream_t stream) {
-  const size_t smem = attn_smem_bytes(NC * 64, DV);
-  auto kern = sparse_attn_kernel<NC, DV>;
+  using C = Cfg<MODE>;
+  constexpr size_t smem = sizeof(AttnBarriers) + 1024              // barriers + alignment slack
+                          + (size_t)NC * kPlane64                  // Q
+                          + (size_t)C::kKStages * kPlane64         // K ring
+                          + (size_t)C::kVStages * VShape<DV>::kStageBytes   // V ring
+                          + (size_t)kPBufs * 2 * kPlane64          // P buffers (keys 0-63, 64-127 each)
+                          + (MODE == kWindow ? 0 : 2 * (size_t)kMaxIdx * sizeof(int32_t));   // staged indices, two units
+  static_assert(smem <= 232448, "shared memory of one CTA");
+  auto kern = sparse_attn_kernel<NC, DV, MODE>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
   // The register split must fit in what the CTA launches with, or the increase
@@ -740,31 +1100,25 @@ cudaError_t launch_t(const AttnParams& p, const CUtensorMap& tq, const CUtensorM
   cudaFuncAttributes fa;
   e = cudaFuncGetAttributes(&fa, kern);
   if (e != cudaSuccess) return e;
-  if ((uint32_t)fa.numRegs < kRegsLaunch) return cudaErrorInvalidConfiguration;
-  return launch_pdl(kern, dim3(grid_clusters * 2), dim3(kThreads), smem, stream, tq, tkv, tkv_tile, p);
+  if (C::kSplitRegs && (uint32_t)fa.numRegs < kRegsLaunch) return cudaErrorInvalidConfiguration;
+  return launch_pdl(kern, dim3(grid_clusters * 2), dim3(C::kThreads), smem, stream, tq, tkv, tkv_tile, p);
 }
 
 }  // namespace
 
-size_t attn_smem_bytes(int d_qk, int d_v) {
-  const int nc = d_qk / 64;
-  const int n = d_v >= 256 ? 256 : d_v;
-  const size_t v_stage = (size_t)(n / 128) * kPlane64;
-  size_t b = sizeof(AttnBarriers) + 1024;          // barriers + alignment slack
-  b += (size_t)nc * kPlane64;                      // Q
-  b += (size_t)kKStages * kPlane64;                // K ring
-  b += (size_t)kVStages * v_stage;                 // V ring
-  b += (size_t)kPBufs * 2 * kPlane64;              // P buffers (keys 0-63, 64-127 each)
-  b += 2 * (size_t)kMaxIdx * sizeof(int32_t);      // staged indices, two units
-  return b;
-}
-
 cudaError_t launch_sparse_attn(const AttnParams& p, int d_qk, int d_v, const CUtensorMap& tq,
                                const CUtensorMap& tkv, const CUtensorMap& tkv_tile, int grid_clusters,
                                cudaStream_t stream) {
-  if (d_qk == 576 && d_v == 512) return launch_t<9, 512>(p, tq, tkv, tkv_tile, grid_clusters, stream);
-  if (d_qk == 192 && d_v == 128) return launch_t<3, 128>(p, tq, tkv, tkv_tile, grid_clusters, stream);
-  return cudaErrorInvalidValue;
+  const bool mla = d_qk == 576 && d_v == 512;
+  if (!mla && !(d_qk == 192 && d_v == 128)) return cudaErrorInvalidValue;
+  if (p.codes)
+    return mla ? launch_t<9, 512, kPacked>(p, tq, tkv, tkv_tile, grid_clusters, stream)
+               : launch_t<3, 128, kPacked>(p, tq, tkv, tkv_tile, grid_clusters, stream);
+  if (p.window)
+    return mla ? launch_t<9, 512, kWindow>(p, tq, tkv, tkv_tile, grid_clusters, stream)
+               : launch_t<3, 128, kWindow>(p, tq, tkv, tkv_tile, grid_clusters, stream);
+  return mla ? launch_t<9, 512, kSelected>(p, tq, tkv, tkv_tile, grid_clusters, stream)
+             : launch_t<3, 128, kSelected>(p, tq, tkv, tkv_tile, grid_clusters, stream);
 }
 
 cudaError_t launch_attn_combine(const AttnParams& p, int d_v, cudaStream_t stream) {

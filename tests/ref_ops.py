@@ -120,11 +120,19 @@ def attention(q, rows, valid, d_v, scale):
     return torch.einsum("nhm,nmd->nhd", p, v), lse, p
 
 
-def attention_tolerance(out, p, rows, valid, d_v):
-    """What bf16 costs an attention output: one rounding of the result (2^-8 of it), and one
-    of every probability before the product with the values: each is off by at most 2^-8 of
-    itself, so the weighted sum by 2^-8 sum p |v|.  The normaliser is summed from the
-    unrounded ones.  fp32 sums and exponentials stay below 2^-13 of sum p |v|: logits of
-    magnitude < 64 with relative error 2^-20 each."""
+def attention_tolerance(q, rows, valid, out, lse, p, d_v, scale):
+    """(tolerance of out, of lse) of a bf16 attention against the 64-bit one.
+
+    A logit is a sum of D products in fp32, in any order: off by at most D 2^-24 times the
+    sum of their magnitudes, times the scale; call the largest of a row delta (the exponential
+    and the row sum add 2^-20).  lse is off by at most delta + 2^-20 (1 + |lse|).
+    The output: every probability off by 2 delta of itself and rounded to bf16 once before
+    the product with the values (2^-8), the normaliser summed from the unrounded ones, the
+    result rounded once (2^-8 of it)."""
     v = torch.where(valid[..., None], rows[..., :d_v].double(), 0.0).abs()
-    return 2.0 ** -8 * out.abs() + (2.0 ** -8 + 2.0 ** -13) * torch.einsum("nhm,nmd->nhd", p, v) + 1e-30
+    k = torch.where(valid[..., None], rows.double(), 0.0).abs()
+    size = torch.einsum("nhd,nmd->nhm", q.double().abs(), k).amax(-1) * scale
+    delta = q.shape[-1] * 2.0 ** -24 * size
+    far = 2.0 ** -8 + 2.0 ** -19 + 2 * delta[..., None]
+    tol = 2.0 ** -8 * out.abs() + far * torch.einsum("nhm,nmd->nhd", p, v) + 1e-30
+    return tol, delta + 2.0 ** -20 * (1 + torch.nan_to_num(lse, neginf=0.0).abs())

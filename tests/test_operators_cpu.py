@@ -95,6 +95,71 @@ def test_kv4_refuses_rows(L):
         assert f(ctypes.byref(c), P, 2 ** 30, None, 0, None) == UNSUPPORTED
 
 
+def _k4(**kw):
+    base = dict(H=128, d_qk=576, d_v=512, scale=0.07, q=16, codes=16, scales=16, tail=16)
+    base.update(kw)
+    return dsa.Kv4AttnArgs(**base)
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(q=None), INVALID), (dict(codes=None), INVALID), (dict(scales=None), INVALID), (dict(tail=None), INVALID),
+    (dict(codes=24), INVALID), (dict(scales=24), INVALID), (dict(tail=24), INVALID), (dict(q=24), INVALID),
+    (dict(scale=0.0), INVALID), (dict(scale=float("inf")), INVALID), (dict(H=64), UNSUPPORTED),
+    (dict(d_v=256), UNSUPPORTED),
+])
+def test_kv4_attention_refuses(L, kw, status):
+    a = _k4(**kw)
+    assert L.dsa_sparse_attn_kv4(ctypes.byref(a), 1, 1, 8, P, 8, P, None, P, 1 << 40, None) == status
+    ia = dsa.IndexerArgs(1, 8, 8, 0, 64, 128, 16, None, 16, 16, None)
+    assert L.dsa_forward_kv4(ctypes.byref(ia), ctypes.byref(a), 8, P, None, P, None, P, 1 << 40, None) == status
+
+
+def test_kv4_attention_refuses_the_rest(L):
+    a = _k4()
+    f = L.dsa_sparse_attn_kv4
+    assert f(None, 1, 1, 8, P, 8, P, None, P, 1 << 40, None) == INVALID
+    for sizes in ((0, 1, 8), (1, 0, 8), (1, 1, 0)):
+        assert f(ctypes.byref(a), *sizes, P, 8, P, None, P, 1 << 40, None) == INVALID
+    assert f(ctypes.byref(a), 2 ** 16, 1, 2 ** 15, P, 8, P, None, P, 1 << 40, None) == UNSUPPORTED
+    assert f(ctypes.byref(a), 1, 1, 8, None, 8, P, None, P, 1 << 40, None) == INVALID
+    assert f(ctypes.byref(a), 1, 1, 8, P, 8, None, None, P, 1 << 40, None) == INVALID
+    assert f(ctypes.byref(a), 1, 1, 8, P, 8, P, ODD, P, 1 << 40, None) == INVALID
+    assert f(ctypes.byref(a), 1, 1, 8, P, 0, P, None, P, 1 << 40, None) == UNSUPPORTED
+    assert f(ctypes.byref(a), 1, 1, 8, P, 2049, P, None, P, 1 << 40, None) == UNSUPPORTED
+    need = dsa.workspace_size(dsa.OP_SPARSE_ATTN, 1, 1, 4096, 2048, 128, 512)
+    assert need > 0 and f(ctypes.byref(a), 1, 1, 4096, P, 2048, P, None, P, need - 1, None) == WORKSPACE
+    assert f(ctypes.byref(a), 1, 1, 4096, P, 2048, P, None, None, need, None) == WORKSPACE
+    ia = dsa.IndexerArgs(1, 8, 8, 0, 64, 128, 16, None, 16, 16, None)
+    assert L.dsa_forward_kv4(ctypes.byref(ia), None, 8, P, None, P, None, P, 1 << 40, None) == INVALID
+    assert L.dsa_forward_kv4(None, ctypes.byref(a), 8, P, None, P, None, P, 1 << 40, None) == INVALID
+    assert L.dsa_forward_kv4(ctypes.byref(ia), ctypes.byref(a), 8, P, None, P, None, P, 255, None) == WORKSPACE
+
+
+def test_window_attention_refuses(L):
+    good = dsa.AttnArgs(128, 576, 512, 0.07, 16, 16)
+    f = L.dsa_window_attn
+
+    def call(a=good, B=1, Lq=4, Lk=8, off=0, start=None, window=4, sinks=0, out=P, lse=None, ws=P, n=1 << 40):
+        return f(None if a is None else ctypes.byref(a), B, Lq, Lk, off, start, window, sinks, out, lse, ws, n, None)
+
+    assert call(a=None) == INVALID and call(out=None) == INVALID and call(out=ODD) == INVALID
+    assert call(lse=ODD) == INVALID and call(start=ODD) == INVALID
+    assert call(B=0) == INVALID and call(Lq=0) == INVALID and call(Lk=0) == INVALID
+    assert call(window=0) == INVALID and call(window=-1) == INVALID and call(sinks=-1) == INVALID
+    assert call(off=5) == INVALID and call(off=-1) == INVALID and call(Lq=9, start=P) == INVALID
+    assert call(a=dsa.AttnArgs(128, 576, 512, 0.07, None, 16)) == INVALID
+    assert call(a=dsa.AttnArgs(64, 576, 512, 0.07, 16, 16)) == UNSUPPORTED
+    assert call(B=2 ** 16, Lk=2 ** 15) == UNSUPPORTED
+    need = dsa.workspace_size(dsa.OP_WINDOW_ATTN, 1, 4, 4096, 1000, 128, 512)
+    assert need > 0 and call(Lk=4096, window=1000, n=need - 1) == WORKSPACE
+    assert call(Lk=4096, window=1000, ws=None, n=need) == WORKSPACE
+    # longer windows than the index lists' 2048 entries, and never more than the keys there are
+    assert dsa.workspace_size(dsa.OP_WINDOW_ATTN, 1, 1, 65536, 40000, 128, 512) > 0
+    assert dsa.workspace_size(dsa.OP_WINDOW_ATTN, 1, 4, 1000, 2 ** 31 - 1, 128, 512) == \
+        dsa.workspace_size(dsa.OP_WINDOW_ATTN, 1, 4, 1000, 1000, 128, 512)
+    assert dsa.workspace_size(dsa.OP_WINDOW_ATTN, 1, 4096, 4096, 512, 128, 512) == 0
+
+
 def test_binding_refuses_tensors_that_are_not_on_a_gpu():
     x = torch.zeros(1, 2, 3, 64, dtype=torch.bfloat16)
     with pytest.raises(ValueError):
