@@ -383,6 +383,8 @@ def indexer_kl_loss_selected(q, kv, indices, lse, sel_scores, d_v, scale, target
 
 def _need_at(t, dtype, shape, name, device):
     """_need, and on the same device as the call's other tensors."""
+    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.device == device and t.is_contiguous():
+        return
     _need(t, dtype, shape, name)
     if t.device != device:
         raise ValueError(f"{name} is on {t.device}, expected {device}")
@@ -393,7 +395,7 @@ def _on(device, stream, call):
     the stream that it launches on (a workspace freed on return is then reused in that
     stream's order)."""
     if stream is None and device.index == torch.cuda.current_device():
-        return call(ctypes.c_void_p(torch.cuda.current_stream().cuda_stream))
+        return call(torch._C._cuda_getCurrentRawStream(device.index))
     if stream is not None and stream.device != device:
         raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
     with torch.cuda.device(device):
@@ -415,26 +417,29 @@ def _norm_rope_args(x, inv_freq, weight, bias, norm, norm_dim, eps, rot_start, i
         raise ValueError(f"norm {norm!r}: expected None, 'rms' or 'layer'")
     dev = x.device
     B, L, H, D = x.shape
-    a = NormRopeArgs(B, L, H, D, x.stride(0), x.stride(1), x.stride(2), x.data_ptr())
-    a.norm, a.eps = _NORMS[norm], float(eps)
+    w_ptr = b_ptr = f_ptr = pos_ptr = None
+    n_freq = w_bf16 = 0
     if norm is not None:
-        a.norm_dim = D if norm_dim is None else int(norm_dim)
-        wt = weight.dtype if isinstance(weight, torch.Tensor) and weight.dtype == torch.bfloat16 else torch.float32
-        _need_at(weight, wt, (a.norm_dim,), "weight", dev)
-        a.weight, a.weight_bf16 = weight.data_ptr(), int(wt == torch.bfloat16)
+        norm_dim = D if norm_dim is None else int(norm_dim)
+        w_bf16 = isinstance(weight, torch.Tensor) and weight.dtype is torch.bfloat16
+        wt = torch.bfloat16 if w_bf16 else torch.float32
+        _need_at(weight, wt, (norm_dim,), "weight", dev)
+        w_ptr = weight.data_ptr()
         if bias is not None:
-            _need_at(bias, wt, (a.norm_dim,), "bias", dev)
-            a.bias = bias.data_ptr()
+            _need_at(bias, wt, (norm_dim,), "bias", dev)
+            b_ptr = bias.data_ptr()
     elif weight is not None or bias is not None or norm_dim is not None:
         raise ValueError("weight, bias and norm_dim belong to a norm")
-    a.rot_start, a.interleaved, a.q_offset = int(rot_start), int(bool(interleaved)), int(q_offset)
     if inv_freq is not None:
-        _need_at(inv_freq, torch.float32, (inv_freq.numel(),), "inv_freq", dev)
-        a.n_freq, a.inv_freq = inv_freq.numel(), inv_freq.data_ptr()
+        n_freq = inv_freq.numel()
+        _need_at(inv_freq, torch.float32, (n_freq,), "inv_freq", dev)
+        f_ptr = inv_freq.data_ptr()
     if positions is not None:
         _need_at(positions, torch.int32, (B, L), "positions", dev)
-        a.positions = positions.data_ptr()
-    return a
+        pos_ptr = positions.data_ptr()
+    sb, sl, sh, _ = x.stride()
+    return NormRopeArgs(B, L, H, D, sb, sl, sh, x.data_ptr(), _NORMS[norm], norm_dim or 0, eps, w_ptr, b_ptr, w_bf16,
+                        rot_start, n_freq, bool(interleaved), f_ptr, pos_ptr, q_offset)
 
 
 def norm_rope(x, inv_freq=None, *, weight=None, bias=None, norm=None, norm_dim=None, eps=1e-6, rot_start=0,

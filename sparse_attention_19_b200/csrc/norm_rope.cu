@@ -13,15 +13,16 @@
 //   g = dz w;  dx = r (g - xhat mean(g xhat) [- mean(g): layer norm]),  dx = dz behind
 //   norm_dim;  dw = sum over rows of dz xhat,  db = sum of dz.
 //
-// Both are bound by HBM: 2 bytes read and 1 or 2 written per element (gradient: 4 read,
-// 2 written) against some 20 fp32 operations.  G lanes hold a row (16-byte vectors, N per
-// lane), so a row's sums are shuffles within G lanes; every group has R rows in flight
-// so that a block of 256 threads keeps 16 KB of loads outstanding.  The angles of a
-// block's tokens are computed once (64-bit range reduction, so a position of 2^31 is as
-// exact as a small one) into shared memory while those loads are in flight; all heads of
-// a token share them.  The other half of a rotated pair is loaded again (an L1 hit)
-// instead of exchanged between lanes: the pairing then works for any split of a row over
-// lanes.
+// Both are bound by HBM (2 bytes read and 1 or 2 written per element; gradient: 4 read, 2
+// written), but at these widths only if the arithmetic stays below ~70 issued
+// instructions per 8 elements, so:
+//   * G lanes hold a head row in 16-byte vectors, and a lane holds BOTH vectors of a rotated
+//     pair (NP pair slots, NM slots for the columns that are not rotated): the rotation needs no
+//     exchange between lanes and every column is normalised once;
+//   * arithmetic runs on packed fp32 pairs (two per instruction);
+//   * the angles of a block's tokens are computed once (64-bit range reduction, so a
+//     position of 2^31 is as exact as a small one) into shared memory while the rows' loads are
+//     in flight; all heads of a token share them.
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>
@@ -37,31 +38,45 @@ namespace dsa {
 
 namespace {
 
-constexpr int kThreads = 256;
-constexpr uint32_t kAmaxFloor = 0x0DA24260u;   // bits of 1e-30f: an all-zero token keeps a positive scale
+constexpr int kMaxThreads = 512;
+constexpr float kAmaxFloor = 1e-30f;           // an all-zero token keeps a positive scale
 
 struct Vec8 {
-  float v[8];
+  float2 v[4];
 };
+
+__device__ __forceinline__ float2 fmul2(float2 a, float2 b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;"
+      : "=l"(r)
+      : "l"(*reinterpret_cast<const uint64_t*>(&a)), "l"(*reinterpret_cast<const uint64_t*>(&b)));
+  return *reinterpret_cast<const float2*>(&r);
+}
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
+
+// max(m, |x|), NaN if either is.
+__device__ __forceinline__ float max_abs(float m, float x) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(m), "f"(fabsf(x)));
+  return r;
+}
 
 __device__ __forceinline__ Vec8 unpack8(const uint4& u) {
   Vec8 r;
   const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    r.v[2 * i] = __uint_as_float(w[i] << 16);
-    r.v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-  }
+  for (int i = 0; i < 4; ++i)
+    r.v[i] = make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
   return r;
 }
 
-__device__ __forceinline__ uint32_t pack2(float a, float b) {
-  const __nv_bfloat162 p = __floats2bfloat162_rn(a, b);
+__device__ __forceinline__ uint32_t pack2(float2 a) {
+  const __nv_bfloat162 p = __float22bfloat162_rn(a);
   return *reinterpret_cast<const uint32_t*>(&p);
 }
 
 __device__ __forceinline__ uint4 pack8(const Vec8& a) {
-  return make_uint4(pack2(a.v[0], a.v[1]), pack2(a.v[2], a.v[3]), pack2(a.v[4], a.v[5]), pack2(a.v[6], a.v[7]));
+  return make_uint4(pack2(a.v[0]), pack2(a.v[1]), pack2(a.v[2]), pack2(a.v[3]));
 }
 
 // 8 parameters from column c (16-byte aligned in either type).
@@ -70,8 +85,8 @@ __device__ __forceinline__ Vec8 load_param8(const void* w, int is_bf16, int c) {
   Vec8 r;
   const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(w) + c);
   const float4 a = __ldg(p), b = __ldg(p + 1);
-  r.v[0] = a.x; r.v[1] = a.y; r.v[2] = a.z; r.v[3] = a.w;
-  r.v[4] = b.x; r.v[5] = b.y; r.v[6] = b.z; r.v[7] = b.w;
+  r.v[0] = make_float2(a.x, a.y); r.v[1] = make_float2(a.z, a.w);
+  r.v[2] = make_float2(b.x, b.y); r.v[3] = make_float2(b.z, b.w);
   return r;
 }
 
@@ -82,219 +97,225 @@ __device__ __forceinline__ float group_sum(float x) {
   return x;
 }
 
-// cos and sin of the tokens [tok0, tok0 + ntok) for every frequency.  Entry j of a token
-// sits at (j % 8) * (F / 8) + j / 8, so that lanes with neighbouring vectors read
-// neighbouring words.
+// Which vectors of a row a lane holds.  Slots 2n and 2n + 1 (n < NP) are the two members
+// of pair vector n * G + lane of the rotated range, the other slots its share of the rest.
+// Without a rotation the "range" is the row's first vectors, so that no slot is wasted.
+template <int G, int NP, int NM>
+struct Slots {
+  static constexpr int kN = 2 * NP + NM;
+  int vec[kN];               // -1: none
+  __device__ __forceinline__ Slots(const NormRopeParams& p, int lane) {
+    const int nv = p.D / 8;
+    const int V = p.n_freq ? p.n_freq / 8 : min(G * NP, nv / 2), rs = p.rot_start / 8;
+#pragma unroll
+    for (int n = 0; n < NP; ++n) {
+      const int i = n * G + lane;
+      vec[2 * n] = i < V ? rs + i : -1;
+      vec[2 * n + 1] = i < V ? rs + V + i : -1;
+    }
+#pragma unroll
+    for (int n = 0; n < NM; ++n) {
+      int i = n * G + lane;
+      if (i >= rs) i += 2 * V;
+      vec[2 * NP + n] = i < nv ? i : -1;
+    }
+  }
+};
+
+// cos and sin of the tokens [tok0, tok0 + ntok) for every frequency.
 __device__ __forceinline__ void fill_angles(const NormRopeParams& p, int tok0, int ntok, float* cs, float* sn) {
-  const int F = p.n_freq, V = F / 8;
-  for (int x = threadIdx.x; x < ntok * F; x += blockDim.x) {
-    const int tl = x / F, j = x - tl * F;
+  for (int x = threadIdx.x; x < ntok * p.n_freq; x += blockDim.x) {
+    const int tl = x / p.n_freq, j = x - tl * p.n_freq;
     const int tok = tok0 + tl;
     const int pos = p.positions ? __ldg(p.positions + tok) : p.q_offset + tok % p.L;
     const double turns = (double)pos * ((double)__ldg(p.inv_freq + j) * 0.15915494309189533577);
-    const float part = (float)(turns - rint(turns));
     float s, c;
-    sincospif(2.f * part, &s, &c);
-    const int at = tl * F + (j & 7) * V + (j >> 3);
-    cs[at] = c;
-    sn[at] = s;
+    sincospif(2.f * (float)(turns - rint(turns)), &s, &c);
+    cs[x] = c;
+    sn[x] = s;
   }
 }
 
-// Where vector `vec` of a row lies in the rotated range.
-struct RotSpot {
-  bool in;        // inside the rotated range
-  bool second;    // half-split: the b member of the pairs
-  int partner;    // half-split: vector that holds the other member
-  int j8;         // first frequency / 8 (half-split), / 4 (interleaved: 4 frequencies a vector)
-};
-__device__ __forceinline__ RotSpot rot_spot(const NormRopeParams& p, int vec) {
-  RotSpot r;
-  const int v = vec - p.rot_start / 8, V = p.n_freq / 8;
-  r.in = p.n_freq > 0 && v >= 0 && v < 2 * V;
-  r.second = v >= V;
-  r.partner = r.second ? vec - V : vec + V;
-  r.j8 = p.interleaved ? v : (r.second ? v - V : v);
+__device__ __forceinline__ Vec8 load_angles(const float* t) {
+  Vec8 r;
+  const float4 a = reinterpret_cast<const float4*>(t)[0], b = reinterpret_cast<const float4*>(t)[1];
+  r.v[0] = make_float2(a.x, a.y); r.v[1] = make_float2(a.z, a.w);
+  r.v[2] = make_float2(b.x, b.y); r.v[3] = make_float2(b.z, b.w);
   return r;
 }
 
-// y = z turned by the token's angles; `sign` -1 turns back.  `o` is the other member's
-// vector (half-split only).
-__device__ __forceinline__ Vec8 rotate8(const NormRopeParams& p, const RotSpot& s, const Vec8& z, const Vec8& o,
-                                        const float* cs, const float* sn, float sign) {
-  const int V = p.n_freq / 8;
-  Vec8 y;
-  if (p.interleaved) {
-    // vector v holds pairs 4v .. 4v+3; frequency j sits at (j % 8) * V + j / 8
+// Turns pair vector i (its members a and b) by the token's angles; `sign` -1 turns back.
+// Interleaved rows keep a pair in two neighbouring columns of one vector: frequencies
+// 8 (i / 2) + 4 (i % 2) .. for a vector i of the range, and likewise for b's.
+__device__ __forceinline__ void rotate_pair(const NormRopeParams& p, int i, Vec8& a, Vec8& b, const float* cs,
+                                            const float* sn, float sign) {
+  if (!p.interleaved) {
+    const Vec8 c = load_angles(cs + 8 * i), s = load_angles(sn + 8 * i);
+    const float2 plus = both(sign), minus = both(-sign);
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      const int j = s.j8 * 4 + e;
-      const float c = cs[(j & 7) * V + (j >> 3)], t = sign * sn[(j & 7) * V + (j >> 3)];
-      y.v[2 * e] = z.v[2 * e] * c - z.v[2 * e + 1] * t;
-      y.v[2 * e + 1] = z.v[2 * e + 1] * c + z.v[2 * e] * t;
+      const float2 x = a.v[e], y = b.v[e];
+      a.v[e] = ffma2(x, c.v[e], fmul2(fmul2(minus, s.v[e]), y));
+      b.v[e] = ffma2(y, c.v[e], fmul2(fmul2(plus, s.v[e]), x));
     }
   } else {
-    const float flip = s.second ? sign : -sign;
+    const int V = p.n_freq / 8;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) y.v[e] = z.v[e] * cs[e * V + s.j8] + o.v[e] * (flip * sn[e * V + s.j8]);
+    for (int m = 0; m < 2; ++m) {
+      Vec8& z = m ? b : a;
+      const int j = 4 * (m ? V + i : i);
+      const float4 c = *reinterpret_cast<const float4*>(cs + j), s = *reinterpret_cast<const float4*>(sn + j);
+      const float cc[4] = {c.x, c.y, c.z, c.w}, ss[4] = {s.x, s.y, s.z, s.w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float2 x = z.v[e];
+        const float t = sign * ss[e];
+        z.v[e] = make_float2(x.x * cc[e] - x.y * t, x.y * cc[e] + x.x * t);
+      }
+    }
   }
-  return y;
 }
 
-// Mean and 1/std of a row held by G lanes.
+// Mean and 1/std of the norm_dim leading columns of a row held by G lanes.
 template <int G, int N>
-__device__ __forceinline__ void row_stats(const NormRopeParams& p, const uint4 (&raw)[N], int lane, float& mean,
-                                          float& rstd) {
+__device__ __forceinline__ void row_stats(const NormRopeParams& p, const uint4 (&raw)[N], const int (&vec)[N],
+                                          float& mean, float& rstd) {
   mean = 0.f;
   rstd = 1.f;
   if (p.norm == DSA_NORM_NONE) return;
   const float inv_n = 1.f / (float)p.norm_dim;
   if (p.norm == DSA_NORM_LAYER) {
-    float s = 0.f;
+    float2 s = both(0.f);
 #pragma unroll
     for (int n = 0; n < N; ++n) {
       const Vec8 x = unpack8(raw[n]);
-      if ((n * G + lane) * 8 < p.norm_dim)
+      if (vec[n] * 8 < p.norm_dim)                       // a missing vector was loaded as zeros
 #pragma unroll
-        for (int e = 0; e < 8; ++e) s += x.v[e];
+        for (int e = 0; e < 4; ++e) s = fadd2(s, x.v[e]);
     }
-    mean = group_sum<G>(s) * inv_n;
+    mean = group_sum<G>(s.x + s.y) * inv_n;
   }
-  float q = 0.f;
+  float2 q = both(0.f);
+  const float2 nm = both(-mean);
 #pragma unroll
   for (int n = 0; n < N; ++n) {
     const Vec8 x = unpack8(raw[n]);
-    if ((n * G + lane) * 8 < p.norm_dim)
+    if (vec[n] >= 0 && vec[n] * 8 < p.norm_dim)
 #pragma unroll
-      for (int e = 0; e < 8; ++e) q = fmaf(x.v[e] - mean, x.v[e] - mean, q);
+      for (int e = 0; e < 4; ++e) {
+        const float2 d = fadd2(x.v[e], nm);
+        q = ffma2(d, d, q);
+      }
   }
-  rstd = rsqrtf(group_sum<G>(q) * inv_n + p.eps);
+  rstd = rsqrtf(group_sum<G>(q.x + q.y) * inv_n + p.eps);
 }
 
-// Rows of one block: tokens [tok0, tok0 + ntok), all heads, in steps of R rows per group.
-template <int G, int N, int R, bool E4M3>
-__global__ void __launch_bounds__(kThreads) norm_rope_kernel(const NormRopeParams p) {
-  constexpr int kGroups = kThreads / G;
-  extern __shared__ float smem[];
+// Rows of one block: tokens [tok0, tok0 + ntok), all heads, one row per group and step.
+template <int G, int NP, int NM, bool E4M3>
+__global__ void __launch_bounds__(E4M3 ? kMaxThreads : 256, (2 * NP + NM) > 4 ? 1 : E4M3 ? 2 : 3)
+norm_rope_kernel(const NormRopeParams p) {
+  using S = Slots<G, NP, NM>;
+  constexpr int N = S::kN;
+  extern __shared__ __align__(16) float smem[];
   float* cs = smem;
   float* sn = cs + p.tokens_per_block * p.n_freq;
-  uint32_t* amax = reinterpret_cast<uint32_t*>(sn + p.tokens_per_block * p.n_freq);   // per token (e4m3)
+  float* amax = sn + p.tokens_per_block * p.n_freq;      // per token (e4m3)
+  const int groups = blockDim.x / G;
   const int lane = threadIdx.x % G, group = threadIdx.x / G;
   const int tok0 = (int)blockIdx.x * p.tokens_per_block;
   const int ntok = min(p.tokens_per_block, p.n_tokens - tok0);
   const int rows = ntok * p.H;
-  const int steps = (rows + kGroups * R - 1) / (kGroups * R);
+  const int steps = (rows + groups - 1) / groups;
+  const S slots(p, lane);
   griddep_launch_dependents();
   griddep_wait();
   if (E4M3)
-    for (int t = threadIdx.x; t < ntok; t += kThreads) amax[t] = kAmaxFloor;
+    for (int t = threadIdx.x; t < ntok; t += blockDim.x) amax[t] = kAmaxFloor;
 
-  uint4 raw[R][N], other[R][N];
-  float y[R][N][8];
   // e4m3 needs the token's maximum before its first code.  A block whose rows fit one step
   // keeps them in registers; a token of more rows is computed twice, the second time
   // from L2.
   const int passes = (E4M3 && steps > 1) ? 2 : 1;
   for (int pass = 0; pass < passes; ++pass) {
     for (int st = 0; st < steps; ++st) {
-#pragma unroll
-      for (int i = 0; i < R; ++i) {
-        const int row = st * kGroups * R + i * kGroups + group;
-        const int tl = row < rows ? row / p.H : 0, h = row < rows ? row - tl * p.H : 0;
+      const int row = st * groups + group;
+      const bool here = row < rows;
+      const int tl = here ? row / p.H : 0, h = here ? row - tl * p.H : 0;
+      uint4 raw[N];
+      {
         const int tok = tok0 + tl, b = tok / p.L, l = tok - b * p.L;
-        const __nv_bfloat16* src = p.x + b * p.stride_b + l * p.stride_l + h * p.stride_h;
+        const uint4* src = reinterpret_cast<const uint4*>(p.x + b * p.stride_b + l * p.stride_l + h * p.stride_h);
 #pragma unroll
-        for (int n = 0; n < N; ++n) {
-          const int vec = n * G + lane;
-          raw[i][n] = other[i][n] = make_uint4(0, 0, 0, 0);
-          if (row < rows && vec * 8 < p.D) {
-            raw[i][n] = __ldg(reinterpret_cast<const uint4*>(src) + vec);
-            const RotSpot s = rot_spot(p, vec);
-            if (s.in && !p.interleaved) other[i][n] = __ldg(reinterpret_cast<const uint4*>(src) + s.partner);
-          }
-        }
+        for (int n = 0; n < N; ++n)
+          raw[n] = here && slots.vec[n] >= 0 ? __ldg(src + slots.vec[n]) : make_uint4(0, 0, 0, 0);
       }
       if (pass == 0 && st == 0) {
         fill_angles(p, tok0, ntok, cs, sn);
         __syncthreads();
       }
-      float mean[R], rstd[R];
-#pragma unroll
-      for (int i = 0; i < R; ++i) row_stats<G, N>(p, raw[i], lane, mean[i], rstd[i]);
+      float mean, rstd;
+      row_stats<G, N>(p, raw, slots.vec, mean, rstd);
+      Vec8 y[N];
 #pragma unroll
       for (int n = 0; n < N; ++n) {
-        const int vec = n * G + lane;
-        const RotSpot s = rot_spot(p, vec);
-        const bool normed = p.norm != DSA_NORM_NONE && vec * 8 < p.norm_dim;
-        const bool onormed = p.norm != DSA_NORM_NONE && s.in && s.partner * 8 < p.norm_dim;
-        Vec8 w{}, bias{}, ow{}, obias{};
-        if (normed) {
-          w = load_param8(p.w, p.w_bf16, vec * 8);
-          if (p.b) bias = load_param8(p.b, p.w_bf16, vec * 8);
-        }
-        if (onormed && !p.interleaved) {
-          ow = load_param8(p.w, p.w_bf16, s.partner * 8);
-          if (p.b) obias = load_param8(p.b, p.w_bf16, s.partner * 8);
-        }
+        y[n] = unpack8(raw[n]);
+        if (p.norm != DSA_NORM_NONE && slots.vec[n] >= 0 && slots.vec[n] * 8 < p.norm_dim) {
+          const Vec8 w = load_param8(p.w, p.w_bf16, slots.vec[n] * 8);
+          const float2 r = both(rstd), nm = both(-mean);
 #pragma unroll
-        for (int i = 0; i < R; ++i) {
-          const int row = st * kGroups * R + i * kGroups + group;
-          const int tl = row < rows ? row / p.H : 0;
-          Vec8 z = unpack8(raw[i][n]), o = unpack8(other[i][n]);
-          if (normed)
+          for (int e = 0; e < 4; ++e) y[n].v[e] = fmul2(fmul2(fadd2(y[n].v[e], nm), r), w.v[e]);
+          if (p.b) {
+            const Vec8 bias = load_param8(p.b, p.w_bf16, slots.vec[n] * 8);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) z.v[e] = fmaf((z.v[e] - mean[i]) * rstd[i], w.v[e], bias.v[e]);
-          if (onormed)
-#pragma unroll
-            for (int e = 0; e < 8; ++e) o.v[e] = fmaf((o.v[e] - mean[i]) * rstd[i], ow.v[e], obias.v[e]);
-          if (s.in) z = rotate8(p, s, z, o, cs + tl * p.n_freq, sn + tl * p.n_freq, 1.f);
-          if (!E4M3) {
-            if (row < rows && vec * 8 < p.D)
-              *reinterpret_cast<uint4*>(p.out + ((size_t)tok0 * p.H + row) * p.D + vec * 8) = pack8(z);
-          } else {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) y[i][n][e] = z.v[e];
+            for (int e = 0; e < 4; ++e) y[n].v[e] = fadd2(y[n].v[e], bias.v[e]);
           }
         }
       }
-      if (E4M3 && pass == 0) {
-        // Maximum of |y| as integers: it does not depend on the order, and a NaN wins.
+      if (p.n_freq) {
 #pragma unroll
-        for (int i = 0; i < R; ++i) {
-          const int row = st * kGroups * R + i * kGroups + group;
-          uint32_t m = 0;
+        for (int n = 0; n < NP; ++n)
+          if (slots.vec[2 * n] >= 0)
+            rotate_pair(p, n * G + lane, y[2 * n], y[2 * n + 1], cs + tl * p.n_freq, sn + tl * p.n_freq, 1.f);
+      }
+      if (!E4M3) {
+        uint4* dst = reinterpret_cast<uint4*>(p.out + ((size_t)tok0 * p.H + row) * p.D);
+        if (here)
 #pragma unroll
           for (int n = 0; n < N; ++n)
+            if (slots.vec[n] >= 0) dst[slots.vec[n]] = pack8(y[n]);
+        continue;
+      }
+      if (pass == 0) {
+        // The maximum does not depend on the order, and a NaN wins (also as an integer).
+        float m = 0.f;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) m = max(m, __float_as_uint(y[i][n][e]) & 0x7fffffffu);
+        for (int n = 0; n < N; ++n)
 #pragma unroll
-          for (int o = G / 2; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
-          if (lane == 0 && row < rows) atomicMax(&amax[row / p.H], m);
-        }
+          for (int e = 0; e < 4; ++e) m = max_abs(max_abs(m, y[n].v[e].x), y[n].v[e].y);
+        if (!here) m = 0.f;
+        const bool one = p.H >= groups;                  // every row of the step is of one token
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1)
+          if (o < G || one) m = max_abs(m, __shfl_xor_sync(0xffffffffu, m, o));
+        if ((one ? threadIdx.x % 32 : lane) == 0 && here)
+          atomicMax(reinterpret_cast<int*>(&amax[tl]), __float_as_int(m));
         if (st == steps - 1) {
           __syncthreads();
-          for (int t = threadIdx.x; t < ntok; t += kThreads) p.scale[tok0 + t] = __uint_as_float(amax[t]) / 448.f;
+          for (int t = threadIdx.x; t < ntok; t += blockDim.x) p.scale[tok0 + t] = amax[t] / 448.f;
         }
       }
-      if (E4M3 && pass == passes - 1) {
+      if (pass == passes - 1 && here) {
+        // y / scale as y * (1 / scale): at most one fp32 step from the quotient.
+        const float2 inv = both(1.f / (amax[tl] / 448.f));
+        uint2* dst = reinterpret_cast<uint2*>(p.codes + ((size_t)tok0 * p.H + row) * p.D);
 #pragma unroll
-        for (int i = 0; i < R; ++i) {
-          const int row = st * kGroups * R + i * kGroups + group;
-          if (row >= rows) continue;
-          // y / scale as y * (1 / scale): at most one fp32 step from the quotient.
-          const float inv = 1.f / (__uint_as_float(amax[row / p.H]) / 448.f);
+        for (int n = 0; n < N; ++n) {
+          if (slots.vec[n] < 0) continue;
+          uint32_t code[4];
 #pragma unroll
-          for (int n = 0; n < N; ++n) {
-            const int vec = n * G + lane;
-            if (vec * 8 >= p.D) continue;
-            uint32_t code[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              code[e] = __nv_cvt_float2_to_fp8x2(make_float2(y[i][n][2 * e] * inv, y[i][n][2 * e + 1] * inv),
-                                                 __NV_SATFINITE, __NV_E4M3);
-            *reinterpret_cast<uint2*>(p.codes + ((size_t)tok0 * p.H + row) * p.D + vec * 8) =
-                make_uint2(code[0] | (code[1] << 16), code[2] | (code[3] << 16));
-          }
+          for (int e = 0; e < 4; ++e)
+            code[e] = __nv_cvt_float2_to_fp8x2(fmul2(y[n].v[e], inv), __NV_SATFINITE, __NV_E4M3);
+          dst[slots.vec[n]] = make_uint2(code[0] | (code[1] << 16), code[2] | (code[3] << 16));
         }
       }
     }
@@ -304,19 +325,26 @@ __global__ void __launch_bounds__(kThreads) norm_rope_kernel(const NormRopeParam
 // Gradient.  Persistent blocks: each walks its chunks of tokens, keeps the sums for dw
 // and db of its columns in registers, and leaves one partial row per block; a second
 // kernel adds the partial rows in block order, so the result does not depend on timing.
-template <int G, int N, int R>
-__global__ void __launch_bounds__(kThreads) norm_rope_bwd_kernel(const NormRopeParams p) {
-  constexpr int kGroups = kThreads / G;
-  extern __shared__ float smem[];
+constexpr int kBwdThreads = 256;
+
+template <int G, int NP, int NM, bool BIAS>
+__global__ void __launch_bounds__(kBwdThreads, (2 * NP + NM) > 4 ? 1 : 2) norm_rope_bwd_kernel(const NormRopeParams p) {
+  using S = Slots<G, NP, NM>;
+  constexpr int N = S::kN, kGroups = kBwdThreads / G;
+  extern __shared__ __align__(16) float smem[];
   const int table = p.tokens_per_block * p.n_freq;
   const int lane = threadIdx.x % G, group = threadIdx.x / G;
+  const S slots(p, lane);
   griddep_launch_dependents();
   griddep_wait();
-  float dw[N][8], db[N][8];
+  Vec8 dw[N], db[BIAS ? N : 1];
 #pragma unroll
   for (int n = 0; n < N; ++n)
 #pragma unroll
-    for (int e = 0; e < 8; ++e) dw[n][e] = db[n][e] = 0.f;
+    for (int e = 0; e < 4; ++e) {
+      dw[n].v[e] = both(0.f);
+      if (BIAS) db[n].v[e] = both(0.f);
+    }
 
   const int n_chunks = (int)(((long long)p.n_tokens + p.tokens_per_block - 1) / p.tokens_per_block);
   int buf = 0;
@@ -324,27 +352,24 @@ __global__ void __launch_bounds__(kThreads) norm_rope_bwd_kernel(const NormRopeP
     const int tok0 = ch * p.tokens_per_block;
     const int ntok = min(p.tokens_per_block, p.n_tokens - tok0);
     const int rows = ntok * p.H;
-    const int steps = (rows + kGroups * R - 1) / (kGroups * R);
+    const int steps = (rows + kGroups - 1) / kGroups;
     float* cs = smem + buf * 2 * table;         // two tables: the next chunk's may be filled
     float* sn = cs + table;                     // while slower warps still read this one
     for (int st = 0; st < steps; ++st) {
-      uint4 raw[R][N], graw[R][N], other[R][N];
-#pragma unroll
-      for (int i = 0; i < R; ++i) {
-        const int row = st * kGroups * R + i * kGroups + group;
-        const int tl = row < rows ? row / p.H : 0, h = row < rows ? row - tl * p.H : 0;
+      const int row = st * kGroups + group;
+      const bool here = row < rows;
+      const int tl = here ? row / p.H : 0, h = here ? row - tl * p.H : 0;
+      uint4 raw[N], graw[N];
+      {
         const int tok = tok0 + tl, b = tok / p.L, l = tok - b * p.L;
-        const __nv_bfloat16* src = p.x + b * p.stride_b + l * p.stride_l + h * p.stride_h;
-        const __nv_bfloat16* gsrc = p.dy + ((size_t)tok0 * p.H + row) * p.D;
+        const uint4* src = reinterpret_cast<const uint4*>(p.x + b * p.stride_b + l * p.stride_l + h * p.stride_h);
+        const uint4* gsrc = reinterpret_cast<const uint4*>(p.dy + ((size_t)tok0 * p.H + row) * p.D);
 #pragma unroll
         for (int n = 0; n < N; ++n) {
-          const int vec = n * G + lane;
-          raw[i][n] = graw[i][n] = other[i][n] = make_uint4(0, 0, 0, 0);
-          if (row < rows && vec * 8 < p.D) {
-            if (vec * 8 < p.norm_dim) raw[i][n] = __ldg(reinterpret_cast<const uint4*>(src) + vec);
-            graw[i][n] = __ldg(reinterpret_cast<const uint4*>(gsrc) + vec);
-            const RotSpot s = rot_spot(p, vec);
-            if (s.in && !p.interleaved) other[i][n] = __ldg(reinterpret_cast<const uint4*>(gsrc) + s.partner);
+          raw[n] = graw[n] = make_uint4(0, 0, 0, 0);
+          if (here && slots.vec[n] >= 0) {
+            if (slots.vec[n] * 8 < p.norm_dim) raw[n] = __ldg(src + slots.vec[n]);
+            graw[n] = __ldg(gsrc + slots.vec[n]);
           }
         }
       }
@@ -352,73 +377,82 @@ __global__ void __launch_bounds__(kThreads) norm_rope_bwd_kernel(const NormRopeP
         fill_angles(p, tok0, ntok, cs, sn);
         __syncthreads();
       }
+      float mean, rstd;
+      row_stats<G, N>(p, raw, slots.vec, mean, rstd);
+      if (!here) rstd = 0.f;                    // 1/sqrt(eps) may be infinite
+      Vec8 g[N];                                // dz, then dz w
 #pragma unroll
-      for (int i = 0; i < R; ++i) {
-        const int row = st * kGroups * R + i * kGroups + group;
-        const int tl = row < rows ? row / p.H : 0;
-        float mean, rstd;
-        row_stats<G, N>(p, raw[i], lane, mean, rstd);
-        float g[N][8], s1 = 0.f, s2 = 0.f;      // g = dz (behind norm_dim) or dz w; sums of g and g xhat
+      for (int n = 0; n < N; ++n) g[n] = unpack8(graw[n]);
+      if (p.n_freq) {
+#pragma unroll
+        for (int n = 0; n < NP; ++n)
+          if (slots.vec[2 * n] >= 0)
+            rotate_pair(p, n * G + lane, g[2 * n], g[2 * n + 1], cs + tl * p.n_freq, sn + tl * p.n_freq, -1.f);
+      }
+      const float2 r2 = both(rstd), nm = both(-mean);
+      float2 s1 = both(0.f), s2 = both(0.f);    // sums of g and of g xhat
+      if (p.norm != DSA_NORM_NONE) {
 #pragma unroll
         for (int n = 0; n < N; ++n) {
-          const int vec = n * G + lane;
-          const RotSpot s = rot_spot(p, vec);
-          Vec8 dz = unpack8(graw[i][n]);
-          if (s.in) dz = rotate8(p, s, dz, unpack8(other[i][n]), cs + tl * p.n_freq, sn + tl * p.n_freq, -1.f);
-          const bool normed = p.norm != DSA_NORM_NONE && vec * 8 < p.norm_dim;
-          if (normed) {
-            const Vec8 x = unpack8(raw[i][n]), w = load_param8(p.w, p.w_bf16, vec * 8);
+          if (slots.vec[n] < 0 || slots.vec[n] * 8 >= p.norm_dim) continue;
+          const Vec8 x = unpack8(raw[n]), w = load_param8(p.w, p.w_bf16, slots.vec[n] * 8);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              const float xh = (x.v[e] - mean) * rstd;
-              // a row past the end has dz = 0, so it adds nothing
-              dw[n][e] = fmaf(dz.v[e], xh, dw[n][e]);
-              db[n][e] += dz.v[e];
-              g[n][e] = dz.v[e] * w.v[e];
-              s1 += g[n][e];
-              s2 = fmaf(g[n][e], xh, s2);
-            }
-          } else {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) g[n][e] = dz.v[e];
+          for (int e = 0; e < 4; ++e) {
+            const float2 xh = fmul2(fadd2(x.v[e], nm), r2);
+            // a row past the end has dz = 0, so it adds nothing
+            dw[n].v[e] = ffma2(g[n].v[e], xh, dw[n].v[e]);
+            if (BIAS) db[n].v[e] = fadd2(db[n].v[e], g[n].v[e]);
+            g[n].v[e] = fmul2(g[n].v[e], w.v[e]);
+            s1 = fadd2(s1, g[n].v[e]);
+            s2 = ffma2(g[n].v[e], xh, s2);
           }
         }
-        if (p.norm != DSA_NORM_NONE) {
-          const float inv_n = 1.f / (float)p.norm_dim;
-          s2 = group_sum<G>(s2) * inv_n;
-          s1 = p.norm == DSA_NORM_LAYER ? group_sum<G>(s1) * inv_n : 0.f;
-        }
+        const float inv_n = 1.f / (float)p.norm_dim;
+        s2 = both(-group_sum<G>(s2.x + s2.y) * inv_n);
+        s1 = both(p.norm == DSA_NORM_LAYER ? -group_sum<G>(s1.x + s1.y) * inv_n : 0.f);
+      }
+      uint4* dst = reinterpret_cast<uint4*>(p.dx + ((size_t)tok0 * p.H + row) * p.D);
 #pragma unroll
-        for (int n = 0; n < N; ++n) {
-          const int vec = n * G + lane;
-          if (row >= rows || vec * 8 >= p.D) continue;
-          Vec8 d;
-          const bool normed = p.norm != DSA_NORM_NONE && vec * 8 < p.norm_dim;
-          const Vec8 x = unpack8(raw[i][n]);
+      for (int n = 0; n < N; ++n) {
+        if (p.norm != DSA_NORM_NONE && slots.vec[n] * 8 < p.norm_dim) {
+          const Vec8 x = unpack8(raw[n]);
 #pragma unroll
-          for (int e = 0; e < 8; ++e)
-            d.v[e] = normed ? rstd * (g[n][e] - s1 - (x.v[e] - mean) * rstd * s2) : g[n][e];
-          *reinterpret_cast<uint4*>(p.dx + ((size_t)tok0 * p.H + row) * p.D + vec * 8) = pack8(d);
+          for (int e = 0; e < 4; ++e) {
+            const float2 xh = fmul2(fadd2(x.v[e], nm), r2);
+            g[n].v[e] = fmul2(r2, ffma2(xh, s2, fadd2(g[n].v[e], s1)));
+          }
         }
+        if (here && slots.vec[n] >= 0) dst[slots.vec[n]] = pack8(g[n]);
       }
     }
   }
   if (p.norm == DSA_NORM_NONE) return;
-  // Sum the groups of the block, column by column, in group order.
-  float* red = smem;                            // [kGroups][norm_dim]
-  for (int what = 0; what < (p.b ? 2 : 1); ++what) {
+  // Sum the rows of each warp (exchange) and then the warps (shared memory), in a fixed order.
+  float* red = smem;                            // [warps][norm_dim]
+  constexpr int kWarps = kBwdThreads / 32;
+  const int warp = threadIdx.x / 32;
+#pragma unroll
+  for (int what = 0; what < (BIAS ? 2 : 1); ++what) {
     __syncthreads();
 #pragma unroll
     for (int n = 0; n < N; ++n) {
-      const int c = (n * G + lane) * 8;
-      if (c < p.norm_dim)
 #pragma unroll
-        for (int e = 0; e < 8; ++e) red[group * p.norm_dim + c + e] = what ? db[n][e] : dw[n][e];
+      for (int e = 0; e < 4; ++e) {
+        float2 t = what ? db[BIAS ? n : 0].v[e] : dw[n].v[e];
+#pragma unroll
+        for (int o = 16; o >= G; o >>= 1) {
+          t.x += __shfl_xor_sync(0xffffffffu, t.x, o);
+          t.y += __shfl_xor_sync(0xffffffffu, t.y, o);
+        }
+        if (threadIdx.x % 32 < G && slots.vec[n] >= 0 && slots.vec[n] * 8 < p.norm_dim)
+          *reinterpret_cast<float2*>(red + warp * p.norm_dim + slots.vec[n] * 8 + 2 * e) = t;
+      }
     }
     __syncthreads();
-    for (int c = threadIdx.x; c < p.norm_dim; c += kThreads) {
+    for (int c = threadIdx.x; c < p.norm_dim; c += kBwdThreads) {
       float s = 0.f;
-      for (int gi = 0; gi < kGroups; ++gi) s += red[gi * p.norm_dim + c];
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) s += red[w * p.norm_dim + c];
       p.part[((size_t)what * gridDim.x + blockIdx.x) * p.norm_dim + c] = s;
     }
   }
@@ -433,8 +467,11 @@ __global__ void __launch_bounds__(256) norm_rope_sum_kernel(const NormRopeParams
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int c = blockIdx.x * 32 + lane, what = blockIdx.y;
   float s = 0.f;
-  if (c < p.norm_dim)
-    for (int i = warp; i < n_part; i += 8) s += p.part[((size_t)what * n_part + i) * p.norm_dim + c];
+  if (c < p.norm_dim) {
+    const float* src = p.part + (size_t)what * n_part * p.norm_dim + c;
+#pragma unroll 8
+    for (int i = warp; i < n_part; i += 8) s += src[(size_t)i * p.norm_dim];
+  }
   red[warp][lane] = s;
   __syncthreads();
   if (warp == 0 && c < p.norm_dim) {
@@ -443,17 +480,26 @@ __global__ void __launch_bounds__(256) norm_rope_sum_kernel(const NormRopeParams
   }
 }
 
-// Lanes per row, vectors per lane and rows per group for a head of D columns.
-template <typename F>
-cudaError_t by_width(int D, F&& f) {
-  const int nv = D / 8;
-  if (nv <= 8) return f(std::integral_constant<int, 8>{}, std::integral_constant<int, 1>{}, std::integral_constant<int, 4>{});
-  if (nv <= 16) return f(std::integral_constant<int, 16>{}, std::integral_constant<int, 1>{}, std::integral_constant<int, 4>{});
-  if (nv <= 24) return f(std::integral_constant<int, 8>{}, std::integral_constant<int, 3>{}, std::integral_constant<int, 1>{});
-  if (nv <= 32) return f(std::integral_constant<int, 32>{}, std::integral_constant<int, 1>{}, std::integral_constant<int, 4>{});
-  if (nv <= 64) return f(std::integral_constant<int, 32>{}, std::integral_constant<int, 2>{}, std::integral_constant<int, 2>{});
-  if (nv <= 96) return f(std::integral_constant<int, 32>{}, std::integral_constant<int, 3>{}, std::integral_constant<int, 1>{});
-  return f(std::integral_constant<int, 32>{}, std::integral_constant<int, 4>{}, std::integral_constant<int, 1>{});
+// Row split for a head of D columns of which 2F are rotated: the fewest lanes whose slots
+// hold it (most slots per lane: fewest idle lanes and exchange steps), up to 6 slots.
+template <typename Fn>
+cudaError_t by_width(const NormRopeParams& p, Fn&& f) {
+  const int nv = p.D / 8;
+  auto fits = [&](int g, int np, int nm) {
+    const int v = p.n_freq ? p.n_freq / 8 : (g * np < nv / 2 ? g * np : nv / 2);
+    return v <= g * np && nv - 2 * v <= g * nm;
+  };
+#define DSA_TRY_SPLIT(G, NP, NM) \
+  if (fits(G, NP, NM))           \
+  return f(std::integral_constant<int, G>{}, std::integral_constant<int, NP>{}, std::integral_constant<int, NM>{})
+  DSA_TRY_SPLIT(4, 1, 0);
+  DSA_TRY_SPLIT(4, 1, 2);
+  DSA_TRY_SPLIT(4, 1, 4);
+  DSA_TRY_SPLIT(8, 1, 2);
+  DSA_TRY_SPLIT(32, 1, 2);
+  DSA_TRY_SPLIT(32, 2, 4);
+#undef DSA_TRY_SPLIT
+  return cudaErrorInvalidValue;
 }
 
 // Tokens per block: what one step holds, spread over the SMs when there are few tokens,
@@ -470,31 +516,35 @@ int tokens_per_block(const NormRopeParams& p, int rows_per_step, int sms) {
 }  // namespace
 
 cudaError_t launch_norm_rope(NormRopeParams p, int sms, cudaStream_t stream) {
-  return by_width(p.D, [&](auto g, auto n, auto r) {
-    constexpr int G = decltype(g)::value, N = decltype(n)::value, R = decltype(r)::value;
-    p.tokens_per_block = tokens_per_block(p, kThreads / G * R, sms);
+  if (!p.n_freq) p.rot_start = 0;
+  return by_width(p, [&](auto g, auto np, auto nm) {
+    constexpr int G = decltype(g)::value, NP = decltype(np)::value, NM = decltype(nm)::value;
+    // Twice the threads where that lets one step hold all heads of a token (e4m3 needs
+    // them together).
+    const int threads = p.codes && p.H > 256 / G ? 512 : 256;
+    p.tokens_per_block = tokens_per_block(p, threads / G, sms);
     const long long grid = ((long long)p.n_tokens + p.tokens_per_block - 1) / p.tokens_per_block;
     const size_t smem = (size_t)p.tokens_per_block * (p.n_freq * 8 + 4);
-    return launch_pdl(p.codes ? norm_rope_kernel<G, N, R, true> : norm_rope_kernel<G, N, R, false>,
-                      dim3((unsigned)grid), dim3(kThreads), smem, stream, p);
+    return launch_pdl(p.codes ? norm_rope_kernel<G, NP, NM, true> : norm_rope_kernel<G, NP, NM, false>,
+                      dim3((unsigned)grid), dim3(threads), smem, stream, p);
   });
 }
 
 int norm_rope_bwd_blocks(int sms) { return sms * kNormRopeBwdBlocksPerSm; }
 
 cudaError_t launch_norm_rope_bwd(NormRopeParams p, int sms, cudaStream_t stream) {
+  if (!p.n_freq) p.rot_start = 0;
   int grid = 0;
-  const cudaError_t e = by_width(p.D, [&](auto g, auto n, auto r) {
-    constexpr int G = decltype(g)::value, N = decltype(n)::value, R = decltype(r)::value;
-    constexpr int RB = R > 2 ? 2 : R;           // three loads a row: half the rows in flight
-    p.tokens_per_block = tokens_per_block(p, kThreads / G * RB, sms);
+  const cudaError_t e = by_width(p, [&](auto g, auto np, auto nm) {
+    constexpr int G = decltype(g)::value, NP = decltype(np)::value, NM = decltype(nm)::value;
+    p.tokens_per_block = tokens_per_block(p, kBwdThreads / G, sms);
     const long long chunks = ((long long)p.n_tokens + p.tokens_per_block - 1) / p.tokens_per_block;
     const long long most = norm_rope_bwd_blocks(sms);
     grid = (int)(chunks < most ? chunks : most);
     size_t smem = (size_t)p.tokens_per_block * p.n_freq * 16;
-    const size_t red = (size_t)(kThreads / G) * p.norm_dim * 4;
+    const size_t red = (size_t)(kBwdThreads / 32) * p.norm_dim * 4;
     if (red > smem) smem = red;
-    return launch_pdl(norm_rope_bwd_kernel<G, N, RB>, dim3(grid), dim3(kThreads), smem, stream, p);
+    return launch_pdl(p.b ? norm_rope_bwd_kernel<G, NP, NM, true> : norm_rope_bwd_kernel<G, NP, NM, false>, dim3(grid), dim3(kBwdThreads), smem, stream, p);
   });
   if (e != cudaSuccess || p.norm == DSA_NORM_NONE) return e;
   return launch_pdl(norm_rope_sum_kernel, dim3((p.norm_dim + 31) / 32, p.b ? 2 : 1), dim3(256), 0, stream, p, grid);
