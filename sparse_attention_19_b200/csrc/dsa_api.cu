@@ -504,8 +504,11 @@ NormRopeParams norm_rope_params(const dsa_norm_rope_args* a) {
   NormRopeParams p{};
   p.L = a->L; p.H = a->H; p.D = a->D;
   p.n_tokens = a->B * a->L;
+  p.div_h = fast_div((uint32_t)a->H);
+  p.div_l = fast_div((uint32_t)a->L);
   p.norm = a->norm;
   p.norm_dim = a->norm == DSA_NORM_NONE ? 0 : a->norm_dim;
+  p.inv_norm_dim = 1.f / (float)(p.norm_dim > 0 ? p.norm_dim : 1);
   p.eps = a->eps;
   p.w_bf16 = a->weight_bf16 ? 1 : 0;
   p.rot_start = a->rot_start; p.n_freq = a->n_freq;

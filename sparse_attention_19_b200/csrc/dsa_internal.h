@@ -138,7 +138,31 @@ cudaError_t launch_indexer_kl(const KlParams& p, int d_qk, const CUtensorMap& tq
                               int grid_clusters, cudaStream_t stream);
 
 // ---------------------------------------------------------------- norm and rotation of heads
+// n / d for 0 <= n < 2^31: with s = ceil(log2 d) and mul = ceil(2^(31+s) / d) the product
+// n * mul exceeds n * 2^(31+s) / d by less than n * d / d * 2^s / d, too little to reach the
+// next multiple of 2^(31+s).
+struct FastDiv {
+  uint32_t d, mul, shift;   // d == 1: n itself
+#ifdef __CUDACC__
+  __device__ __forceinline__ int operator()(int n) const {
+    return d == 1 ? n : (int)(__umulhi((uint32_t)n, mul) >> shift);
+  }
+#endif
+};
+inline FastDiv fast_div(uint32_t d) {
+  FastDiv f{d, 0, 0};
+  uint32_t s = 0;
+  while (s < 31 && (1u << s) < d) ++s;
+  if (d > 1) {
+    f.mul = (uint32_t)(((1ull << (31 + s)) + d - 1) / d);
+    f.shift = s - 1;
+  }
+  return f;
+}
 struct NormRopeParams {
+  FastDiv div_h, div_l;   // by H and L
+  float inv_norm_dim;
+  int n_chunks;           // set by the launcher
   int L, H, D;            // tokens are (b, l) pairs, b = token / L
   int n_tokens;           // B * L
   int tokens_per_block;   // set by the launcher

@@ -39,6 +39,7 @@ namespace dsa {
 namespace {
 
 constexpr int kMaxThreads = 512;
+constexpr int kNormRopeBlocksPerSm = 4;        // blocks of 256 threads
 constexpr float kAmaxFloor = 1e-30f;           // an all-zero token keeps a positive scale
 
 struct Vec8 {
@@ -127,7 +128,7 @@ __device__ __forceinline__ void fill_angles(const NormRopeParams& p, int tok0, i
   for (int x = threadIdx.x; x < ntok * p.n_freq; x += blockDim.x) {
     const int tl = x / p.n_freq, j = x - tl * p.n_freq;
     const int tok = tok0 + tl;
-    const int pos = p.positions ? __ldg(p.positions + tok) : p.q_offset + tok % p.L;
+    const int pos = p.positions ? __ldg(p.positions + tok) : p.q_offset + tok - p.div_l(tok) * p.L;
     const double turns = (double)pos * ((double)__ldg(p.inv_freq + j) * 0.15915494309189533577);
     float s, c;
     sincospif(2.f * (float)(turns - rint(turns)), &s, &c);
@@ -183,7 +184,7 @@ __device__ __forceinline__ void row_stats(const NormRopeParams& p, const uint4 (
   mean = 0.f;
   rstd = 1.f;
   if (p.norm == DSA_NORM_NONE) return;
-  const float inv_n = 1.f / (float)p.norm_dim;
+  const float inv_n = p.inv_norm_dim;
   if (p.norm == DSA_NORM_LAYER) {
     float2 s = both(0.f);
 #pragma unroll
@@ -210,114 +211,212 @@ __device__ __forceinline__ void row_stats(const NormRopeParams& p, const uint4 (
   rstd = rsqrtf(group_sum<G>(q.x + q.y) * inv_n + p.eps);
 }
 
-// Rows of one block: tokens [tok0, tok0 + ntok), all heads, one row per group and step.
+// z of one vector: normalised (columns below norm_dim), or as it is (zeros for no vector).
+__device__ __forceinline__ Vec8 normed8(const NormRopeParams& p, const uint4& raw, int vec, float mean, float rstd) {
+  Vec8 z = unpack8(raw);
+  if ((unsigned)(vec * 8) < (unsigned)p.norm_dim) {      // norm_dim is 0 without a norm; no vector: -1
+    const Vec8 w = load_param8(p.w, p.w_bf16, vec * 8);
+    const float2 r = both(rstd);
+    if (p.norm == DSA_NORM_LAYER) {
+      const float2 nm = both(-mean);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) z.v[e] = fadd2(z.v[e], nm);
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) z.v[e] = fmul2(fmul2(z.v[e], r), w.v[e]);
+    if (p.b) {
+      const Vec8 bias = load_param8(p.b, p.w_bf16, vec * 8);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) z.v[e] = fadd2(z.v[e], bias.v[e]);
+    }
+  }
+  return z;
+}
+
+__device__ __forceinline__ uint2 to_e4m3(const Vec8& y, float2 inv) {
+  uint32_t code[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) code[e] = __nv_cvt_float2_to_fp8x2(fmul2(y.v[e], inv), __NV_SATFINITE, __NV_E4M3);
+  return make_uint2(code[0] | (code[1] << 16), code[2] | (code[3] << 16));
+}
+
+// 1/scale; y / scale is computed as y * (1 / scale), a few fp32 steps from the quotient at most.
+__device__ __forceinline__ float inv_scale(float amax) { return 1.f / (amax * (1.f / 448.f)); }
+
+// Persistent blocks over chunks of rows, one row per group of G lanes and chunk.  A chunk is
+// tokens_per_block whole tokens, or (bf16 only) `groups` heads of one token.  While a chunk
+// is computed the next one's rows are in flight, and its angles are filled in before the
+// chunk's one barrier; that barrier also completes the tokens' maxima for e4m3.
 template <int G, int NP, int NM, bool E4M3>
-__global__ void __launch_bounds__(E4M3 ? kMaxThreads : 256, (2 * NP + NM) > 4 ? 1 : E4M3 ? 2 : 3)
+__global__ void __launch_bounds__(E4M3 ? kMaxThreads : 256, (2 * NP + NM) > 6 ? 1 : E4M3 ? 1 : 2)
 norm_rope_kernel(const NormRopeParams p) {
   using S = Slots<G, NP, NM>;
   constexpr int N = S::kN;
   extern __shared__ __align__(16) float smem[];
-  float* cs = smem;
-  float* sn = cs + p.tokens_per_block * p.n_freq;
-  float* amax = sn + p.tokens_per_block * p.n_freq;      // per token (e4m3)
+  const int table = p.tokens_per_block * p.n_freq;
+  float* amax3 = smem + 4 * table;                       // three buffers of one value per token (e4m3)
   const int groups = blockDim.x / G;
   const int lane = threadIdx.x % G, group = threadIdx.x / G;
-  const int tok0 = (int)blockIdx.x * p.tokens_per_block;
-  const int ntok = min(p.tokens_per_block, p.n_tokens - tok0);
-  const int rows = ntok * p.H;
-  const int steps = (rows + groups - 1) / groups;
   const S slots(p, lane);
+  const int parts = E4M3 ? 1 : (p.H + groups - 1) / groups;   // chunks of a token that fills more than one
+  // Chunk -> first token, tokens, this group's token in the chunk and head.
+  struct Place { int tok0, ntok, tl, h; bool here; };
+  auto place = [&](int ch) {
+    Place q;
+    if (parts == 1) {
+      q.tok0 = ch * p.tokens_per_block;
+      q.ntok = min(p.tokens_per_block, p.n_tokens - q.tok0);
+      q.tl = p.div_h(group);
+      q.h = group - q.tl * p.H;
+      q.here = q.tl < q.ntok;
+    } else {
+      q.tok0 = ch / parts;
+      q.ntok = 1;
+      q.tl = 0;
+      q.h = (ch - q.tok0 * parts) * groups + group;
+      q.here = q.h < p.H;
+    }
+    if (!q.here) q.tl = q.h = 0;                         // (reads the first token's angles, writes nothing)
+    return q;
+  };
+  uint4 raw[N];
+  auto load = [&](const Place& q) {
+    const int tok = q.tok0 + q.tl, b = p.div_l(tok), l = tok - b * p.L;
+    const uint4* src = reinterpret_cast<const uint4*>(p.x + b * p.stride_b + l * p.stride_l + q.h * p.stride_h);
+#pragma unroll
+    for (int n = 0; n < N; ++n)
+      raw[n] = q.here && slots.vec[n] >= 0 ? __ldg(src + slots.vec[n]) : make_uint4(0, 0, 0, 0);
+  };
   griddep_launch_dependents();
   griddep_wait();
+  int ch = blockIdx.x;
+  Place q = place(ch);
+  load(q);
+  fill_angles(p, q.tok0, q.ntok, smem, smem + table);
   if (E4M3)
-    for (int t = threadIdx.x; t < ntok; t += blockDim.x) amax[t] = kAmaxFloor;
+    for (int t = threadIdx.x; t < p.tokens_per_block; t += blockDim.x) amax3[t] = kAmaxFloor;
+  __syncthreads();
+  for (int it = 0, a3 = 0; ch < p.n_chunks; ch += gridDim.x, it ^= 1) {
+    const float* cs = smem + it * 2 * table;
+    const float* sn = cs + table;
+    float* amax = amax3 + a3 * p.tokens_per_block;
+    a3 = a3 == 2 ? 0 : a3 + 1;
+    float* amax_next = amax3 + a3 * p.tokens_per_block;
+    float mean, rstd;
+    row_stats<G, N>(p, raw, slots.vec, mean, rstd);
+    const size_t row = ((size_t)(q.tok0 + q.tl) * p.H + q.h) * (p.D / 8);   // of the output, in vectors
+    Vec8 y[E4M3 ? N : 1];
+    auto emit = [&](int n, const Vec8& z) {
+      if constexpr (E4M3) y[n] = z;
+      else if (q.here && slots.vec[n] >= 0) reinterpret_cast<uint4*>(p.out)[row + slots.vec[n]] = pack8(z);
+    };
+#pragma unroll
+    for (int n = 0; n < NP; ++n) {
+      Vec8 a = normed8(p, raw[2 * n], slots.vec[2 * n], mean, rstd);
+      Vec8 b = normed8(p, raw[2 * n + 1], slots.vec[2 * n + 1], mean, rstd);
+      if (p.n_freq && slots.vec[2 * n] >= 0)
+        rotate_pair(p, n * G + lane, a, b, cs + q.tl * p.n_freq, sn + q.tl * p.n_freq, 1.f);
+      emit(2 * n, a);
+      emit(2 * n + 1, b);
+    }
+#pragma unroll
+    for (int n = 2 * NP; n < N; ++n) emit(n, normed8(p, raw[n], slots.vec[n], mean, rstd));
 
-  // e4m3 needs the token's maximum before its first code.  A block whose rows fit one step
-  // keeps them in registers; a token of more rows is computed twice, the second time
-  // from L2.
-  const int passes = (E4M3 && steps > 1) ? 2 : 1;
-  for (int pass = 0; pass < passes; ++pass) {
-    for (int st = 0; st < steps; ++st) {
-      const int row = st * groups + group;
-      const bool here = row < rows;
-      const int tl = here ? row / p.H : 0, h = here ? row - tl * p.H : 0;
-      uint4 raw[N];
-      {
-        const int tok = tok0 + tl, b = tok / p.L, l = tok - b * p.L;
-        const uint4* src = reinterpret_cast<const uint4*>(p.x + b * p.stride_b + l * p.stride_l + h * p.stride_h);
+    const Place now = q;
+    if (ch + (int)gridDim.x < p.n_chunks) {
+      q = place(ch + gridDim.x);
+      load(q);
+      float* tab = smem + (it ^ 1) * 2 * table;
+      fill_angles(p, q.tok0, q.ntok, tab, tab + table);
+    }
+    if constexpr (E4M3) {
+      // The maximum does not depend on the order, and a NaN wins (also as an integer).
+      float m = 0.f;
+#pragma unroll
+      for (int n = 0; n < N; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) m = max_abs(max_abs(m, y[n].v[e].x), y[n].v[e].y);
+      if (!now.here) m = 0.f;
+      const bool one = p.H >= 32 / G && p.H % (32 / G) == 0;   // every row of the warp is of one token
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1)
+        if (o < G || one) m = max_abs(m, __shfl_xor_sync(0xffffffffu, m, o));
+      if ((one ? threadIdx.x % 32 : lane) == 0 && now.here)
+        atomicMax(reinterpret_cast<int*>(&amax[now.tl]), __float_as_int(m));
+      for (int t = threadIdx.x; t < p.tokens_per_block; t += blockDim.x) amax_next[t] = kAmaxFloor;
+    }
+    __syncthreads();
+    if constexpr (E4M3) {
+      if (threadIdx.x < now.ntok) p.scale[now.tok0 + threadIdx.x] = amax[threadIdx.x] / 448.f;
+      if (now.here) {
+        const float2 inv = both(inv_scale(amax[now.tl]));
+        uint2* dst = reinterpret_cast<uint2*>(p.codes) + row;
 #pragma unroll
         for (int n = 0; n < N; ++n)
-          raw[n] = here && slots.vec[n] >= 0 ? __ldg(src + slots.vec[n]) : make_uint4(0, 0, 0, 0);
+          if (slots.vec[n] >= 0) dst[slots.vec[n]] = to_e4m3(y[n], inv);
       }
-      if (pass == 0 && st == 0) {
-        fill_angles(p, tok0, ntok, cs, sn);
-        __syncthreads();
-      }
+    }
+  }
+}
+
+// e4m3 of tokens with more heads than a block holds: one block per token, the rows
+// computed twice (the second time from L2), first for the maximum.
+template <int G, int NP, int NM>
+__global__ void __launch_bounds__(kMaxThreads) norm_rope_wide_kernel(const NormRopeParams p) {
+  using S = Slots<G, NP, NM>;
+  constexpr int N = S::kN;
+  extern __shared__ __align__(16) float smem[];
+  __shared__ float amax;
+  float *cs = smem, *sn = smem + p.n_freq;
+  const int groups = blockDim.x / G;
+  const int lane = threadIdx.x % G, group = threadIdx.x / G;
+  const S slots(p, lane);
+  const int tok = blockIdx.x, b = p.div_l(tok), l = tok - b * p.L;
+  griddep_launch_dependents();
+  griddep_wait();
+  if (threadIdx.x == 0) amax = kAmaxFloor;
+  fill_angles(p, tok, 1, cs, sn);
+  __syncthreads();
+  float m = 0.f;
+  for (int pass = 0; pass < 2; ++pass) {
+    for (int h0 = 0; h0 < p.H; h0 += groups) {
+      const int h = h0 + group;
+      const bool here = h < p.H;
+      const uint4* src = reinterpret_cast<const uint4*>(p.x + b * p.stride_b + l * p.stride_l + (here ? h : 0) * p.stride_h);
+      uint4 raw[N];
+#pragma unroll
+      for (int n = 0; n < N; ++n)
+        raw[n] = here && slots.vec[n] >= 0 ? __ldg(src + slots.vec[n]) : make_uint4(0, 0, 0, 0);
       float mean, rstd;
       row_stats<G, N>(p, raw, slots.vec, mean, rstd);
       Vec8 y[N];
 #pragma unroll
-      for (int n = 0; n < N; ++n) {
-        y[n] = unpack8(raw[n]);
-        if (p.norm != DSA_NORM_NONE && slots.vec[n] >= 0 && slots.vec[n] * 8 < p.norm_dim) {
-          const Vec8 w = load_param8(p.w, p.w_bf16, slots.vec[n] * 8);
-          const float2 r = both(rstd), nm = both(-mean);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) y[n].v[e] = fmul2(fmul2(fadd2(y[n].v[e], nm), r), w.v[e]);
-          if (p.b) {
-            const Vec8 bias = load_param8(p.b, p.w_bf16, slots.vec[n] * 8);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) y[n].v[e] = fadd2(y[n].v[e], bias.v[e]);
-          }
-        }
-      }
-      if (p.n_freq) {
+      for (int n = 0; n < N; ++n) y[n] = normed8(p, raw[n], slots.vec[n], mean, rstd);
+      if (p.n_freq)
 #pragma unroll
         for (int n = 0; n < NP; ++n)
-          if (slots.vec[2 * n] >= 0)
-            rotate_pair(p, n * G + lane, y[2 * n], y[2 * n + 1], cs + tl * p.n_freq, sn + tl * p.n_freq, 1.f);
-      }
-      if (!E4M3) {
-        uint4* dst = reinterpret_cast<uint4*>(p.out + ((size_t)tok0 * p.H + row) * p.D);
-        if (here)
-#pragma unroll
-          for (int n = 0; n < N; ++n)
-            if (slots.vec[n] >= 0) dst[slots.vec[n]] = pack8(y[n]);
-        continue;
-      }
+          if (slots.vec[2 * n] >= 0) rotate_pair(p, n * G + lane, y[2 * n], y[2 * n + 1], cs, sn, 1.f);
+      if (!here) continue;
       if (pass == 0) {
-        // The maximum does not depend on the order, and a NaN wins (also as an integer).
-        float m = 0.f;
 #pragma unroll
         for (int n = 0; n < N; ++n)
+          if (slots.vec[n] >= 0)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) m = max_abs(max_abs(m, y[n].v[e].x), y[n].v[e].y);
-        if (!here) m = 0.f;
-        const bool one = p.H >= groups;                  // every row of the step is of one token
+            for (int e = 0; e < 4; ++e) m = max_abs(max_abs(m, y[n].v[e].x), y[n].v[e].y);
+      } else {
+        const float2 inv = both(inv_scale(amax));
+        uint2* dst = reinterpret_cast<uint2*>(p.codes) + ((size_t)tok * p.H + h) * (p.D / 8);
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1)
-          if (o < G || one) m = max_abs(m, __shfl_xor_sync(0xffffffffu, m, o));
-        if ((one ? threadIdx.x % 32 : lane) == 0 && here)
-          atomicMax(reinterpret_cast<int*>(&amax[tl]), __float_as_int(m));
-        if (st == steps - 1) {
-          __syncthreads();
-          for (int t = threadIdx.x; t < ntok; t += blockDim.x) p.scale[tok0 + t] = amax[t] / 448.f;
-        }
+        for (int n = 0; n < N; ++n)
+          if (slots.vec[n] >= 0) dst[slots.vec[n]] = to_e4m3(y[n], inv);
       }
-      if (pass == passes - 1 && here) {
-        // y / scale as y * (1 / scale): at most one fp32 step from the quotient.
-        const float2 inv = both(1.f / (amax[tl] / 448.f));
-        uint2* dst = reinterpret_cast<uint2*>(p.codes + ((size_t)tok0 * p.H + row) * p.D);
+    }
+    if (pass == 0) {
 #pragma unroll
-        for (int n = 0; n < N; ++n) {
-          if (slots.vec[n] < 0) continue;
-          uint32_t code[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            code[e] = __nv_cvt_float2_to_fp8x2(fmul2(y[n].v[e], inv), __NV_SATFINITE, __NV_E4M3);
-          dst[slots.vec[n]] = make_uint2(code[0] | (code[1] << 16), code[2] | (code[3] << 16));
-        }
-      }
+      for (int o = 16; o > 0; o >>= 1) m = max_abs(m, __shfl_xor_sync(0xffffffffu, m, o));
+      if (threadIdx.x % 32 == 0) atomicMax(reinterpret_cast<int*>(&amax), __float_as_int(m));
+      __syncthreads();
+      if (threadIdx.x == 0) p.scale[tok] = amax / 448.f;
     }
   }
 }
@@ -358,10 +457,10 @@ __global__ void __launch_bounds__(kBwdThreads, (2 * NP + NM) > 4 ? 1 : 2) norm_r
     for (int st = 0; st < steps; ++st) {
       const int row = st * kGroups + group;
       const bool here = row < rows;
-      const int tl = here ? row / p.H : 0, h = here ? row - tl * p.H : 0;
+      const int tl = here ? p.div_h(row) : 0, h = here ? row - tl * p.H : 0;
       uint4 raw[N], graw[N];
       {
-        const int tok = tok0 + tl, b = tok / p.L, l = tok - b * p.L;
+        const int tok = tok0 + tl, b = p.div_l(tok), l = tok - b * p.L;
         const uint4* src = reinterpret_cast<const uint4*>(p.x + b * p.stride_b + l * p.stride_l + h * p.stride_h);
         const uint4* gsrc = reinterpret_cast<const uint4*>(p.dy + ((size_t)tok0 * p.H + row) * p.D);
 #pragma unroll
@@ -407,7 +506,7 @@ __global__ void __launch_bounds__(kBwdThreads, (2 * NP + NM) > 4 ? 1 : 2) norm_r
             s2 = ffma2(g[n].v[e], xh, s2);
           }
         }
-        const float inv_n = 1.f / (float)p.norm_dim;
+        const float inv_n = p.inv_norm_dim;
         s2 = both(-group_sum<G>(s2.x + s2.y) * inv_n);
         s1 = both(p.norm == DSA_NORM_LAYER ? -group_sum<G>(s1.x + s1.y) * inv_n : 0.f);
       }
@@ -519,14 +618,20 @@ cudaError_t launch_norm_rope(NormRopeParams p, int sms, cudaStream_t stream) {
   if (!p.n_freq) p.rot_start = 0;
   return by_width(p, [&](auto g, auto np, auto nm) {
     constexpr int G = decltype(g)::value, NP = decltype(np)::value, NM = decltype(nm)::value;
-    // Twice the threads where that lets one step hold all heads of a token (e4m3 needs
-    // them together).
-    const int threads = p.codes && p.H > 256 / G ? 512 : 256;
-    p.tokens_per_block = tokens_per_block(p, threads / G, sms);
-    const long long grid = ((long long)p.n_tokens + p.tokens_per_block - 1) / p.tokens_per_block;
-    const size_t smem = (size_t)p.tokens_per_block * (p.n_freq * 8 + 4);
+    if (p.codes && p.H > kMaxThreads / G)
+      return launch_pdl(norm_rope_wide_kernel<G, NP, NM>, dim3(p.n_tokens), dim3(kMaxThreads),
+                        (size_t)p.n_freq * 8, stream, p);
+    // Twice the threads where that lets a block hold all heads of a token (e4m3).
+    const int threads = p.codes && p.H > 256 / G ? kMaxThreads : 256, groups = threads / G;
+    p.tokens_per_block = tokens_per_block(p, groups, sms);
+    const long long chunks = p.H > groups ? (long long)p.n_tokens * ((p.H + groups - 1) / groups)
+                                          : ((long long)p.n_tokens + p.tokens_per_block - 1) / p.tokens_per_block;
+    if (chunks >= (1ll << 31) - sms * 8) return cudaErrorInvalidValue;
+    p.n_chunks = (int)chunks;
+    const long long most = (long long)sms * (threads == 256 ? kNormRopeBlocksPerSm : kNormRopeBlocksPerSm / 2);
+    const size_t smem = ((size_t)p.tokens_per_block * p.n_freq * 4 + 3 * p.tokens_per_block) * sizeof(float);
     return launch_pdl(p.codes ? norm_rope_kernel<G, NP, NM, true> : norm_rope_kernel<G, NP, NM, false>,
-                      dim3((unsigned)grid), dim3(threads), smem, stream, p);
+                      dim3((unsigned)(chunks < most ? chunks : most)), dim3(threads), smem, stream, p);
   });
 }
 
