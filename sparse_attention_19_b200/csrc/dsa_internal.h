@@ -160,12 +160,13 @@ inline FastDiv fast_div(uint32_t d) {
   return f;
 }
 struct NormRopeParams {
-  FastDiv div_h, div_l;   // by H and L
+  FastDiv div_h, div_l, div_parts;   // by H, L and parts
   float inv_norm_dim;
-  int n_chunks;           // set by the launcher
+  // Set by the launcher: blocks walk spans of span_tokens tokens (whose angles are filled in
+  // together) in steps of tokens_per_step tokens, or of one of `parts` parts of a token's heads.
+  int n_spans, span_tokens, tokens_per_step, parts;
   int L, H, D;            // tokens are (b, l) pairs, b = token / L
   int n_tokens;           // B * L
-  int tokens_per_block;   // set by the launcher
   int norm, norm_dim;     // dsa_norm; columns [0, norm_dim) are normalised
   float eps;
   int w_bf16;             // w and b in bf16 instead of fp32

@@ -39,7 +39,7 @@ namespace dsa {
 namespace {
 
 constexpr int kMaxThreads = 512;
-constexpr int kNormRopeBlocksPerSm = 4;        // blocks of 256 threads
+constexpr int kBlocksPerSm = 4;                // blocks of 256 threads
 constexpr float kAmaxFloor = 1e-30f;           // an all-zero token keeps a positive scale
 
 struct Vec8 {
@@ -177,61 +177,107 @@ __device__ __forceinline__ void rotate_pair(const NormRopeParams& p, int i, Vec8
   }
 }
 
-// Mean and 1/std of the norm_dim leading columns of a row held by G lanes.
-template <int G, int N>
-__device__ __forceinline__ void row_stats(const NormRopeParams& p, const uint4 (&raw)[N], const int (&vec)[N],
-                                          float& mean, float& rstd) {
-  mean = 0.f;
-  rstd = 1.f;
-  if (p.norm == DSA_NORM_NONE) return;
-  const float inv_n = p.inv_norm_dim;
-  if (p.norm == DSA_NORM_LAYER) {
-    float2 s = both(0.f);
-#pragma unroll
-    for (int n = 0; n < N; ++n) {
-      const Vec8 x = unpack8(raw[n]);
-      if (vec[n] * 8 < p.norm_dim)                       // a missing vector was loaded as zeros
-#pragma unroll
-        for (int e = 0; e < 4; ++e) s = fadd2(s, x.v[e]);
-    }
-    mean = group_sum<G>(s.x + s.y) * inv_n;
-  }
-  float2 q = both(0.f);
-  const float2 nm = both(-mean);
-#pragma unroll
-  for (int n = 0; n < N; ++n) {
-    const Vec8 x = unpack8(raw[n]);
-    if (vec[n] >= 0 && vec[n] * 8 < p.norm_dim)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const float2 d = fadd2(x.v[e], nm);
-        q = ffma2(d, d, q);
-      }
-  }
-  rstd = rsqrtf(group_sum<G>(q.x + q.y) * inv_n + p.eps);
+// Whether a vector is normalised (norm_dim is 0 without a norm; no vector: -1).
+__device__ __forceinline__ bool is_normed(const NormRopeParams& p, int vec) {
+  return (unsigned)(vec * 8) < (unsigned)p.norm_dim;
 }
 
-// z of one vector: normalised (columns below norm_dim), or as it is (zeros for no vector).
-__device__ __forceinline__ Vec8 normed8(const NormRopeParams& p, const uint4& raw, int vec, float mean, float rstd) {
-  Vec8 z = unpack8(raw);
-  if ((unsigned)(vec * 8) < (unsigned)p.norm_dim) {      // norm_dim is 0 without a norm; no vector: -1
-    const Vec8 w = load_param8(p.w, p.w_bf16, vec * 8);
-    const float2 r = both(rstd);
-    if (p.norm == DSA_NORM_LAYER) {
-      const float2 nm = both(-mean);
+// x -> xhat = (x - mean) / std over the norm_dim leading columns of a row held by G lanes;
+// returns 1/std.  Columns behind them stay as they are.
+template <int G, bool LAYER, int N>
+__device__ __forceinline__ float normalise(const NormRopeParams& p, Vec8 (&x)[N], const int (&vec)[N]) {
+  if (p.norm == DSA_NORM_NONE) return 1.f;
+  if constexpr (LAYER) {
+    float2 s = both(0.f);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) z.v[e] = fadd2(z.v[e], nm);
-    }
+    for (int n = 0; n < N; ++n)
+      if (is_normed(p, vec[n]))
 #pragma unroll
-    for (int e = 0; e < 4; ++e) z.v[e] = fmul2(fmul2(z.v[e], r), w.v[e]);
-    if (p.b) {
-      const Vec8 bias = load_param8(p.b, p.w_bf16, vec * 8);
+        for (int e = 0; e < 4; ++e) s = fadd2(s, x[n].v[e]);
+    const float2 nm = both(-group_sum<G>(s.x + s.y) * p.inv_norm_dim);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) z.v[e] = fadd2(z.v[e], bias.v[e]);
-    }
+    for (int n = 0; n < N; ++n)
+      if (is_normed(p, vec[n]))
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[n].v[e] = fadd2(x[n].v[e], nm);
   }
-  return z;
+  float2 q = both(0.f);
+#pragma unroll
+  for (int n = 0; n < N; ++n)
+    if (is_normed(p, vec[n]))
+#pragma unroll
+      for (int e = 0; e < 4; ++e) q = ffma2(x[n].v[e], x[n].v[e], q);
+  const float rstd = rsqrtf(group_sum<G>(q.x + q.y) * p.inv_norm_dim + p.eps);
+#pragma unroll
+  for (int n = 0; n < N; ++n)
+    if (is_normed(p, vec[n]))
+#pragma unroll
+      for (int e = 0; e < 4; ++e) x[n].v[e] = fmul2(x[n].v[e], both(rstd));
+  return rstd;
 }
+
+// Weights (and biases behind them) as fp32 in shared memory, norm_dim each.
+__device__ __forceinline__ void fill_params(const NormRopeParams& p, float* w) {
+  for (int c = threadIdx.x * 8; c < p.norm_dim; c += blockDim.x * 8) {
+    *reinterpret_cast<Vec8*>(w + c) = load_param8(p.w, p.w_bf16, c);
+    if (p.b) *reinterpret_cast<Vec8*>(w + p.norm_dim + c) = load_param8(p.b, p.w_bf16, c);
+  }
+}
+
+// z = xhat w + b.
+template <bool LAYER>
+__device__ __forceinline__ void scale8(const NormRopeParams& p, Vec8& z, int vec, const float* w) {
+  if (!is_normed(p, vec)) return;
+  const Vec8 a = load_angles(w + vec * 8);
+  if (LAYER && p.b) {
+    const Vec8 b = load_angles(w + p.norm_dim + vec * 8);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) z.v[e] = ffma2(z.v[e], a.v[e], b.v[e]);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) z.v[e] = fmul2(z.v[e], a.v[e]);
+  }
+}
+
+// Steps of a block: spans blockIdx.x, blockIdx.x + gridDim.x, ... of span_tokens tokens, each in
+// steps of one row per group of lanes: tokens_per_step whole tokens, or part of a token's heads.
+struct Walk {
+  int span, step, steps;    // steps: of this span
+  int tok0, ntok;           // of the span
+  int tl, h;                // this group's row: token in the span and head
+  int first, n;             // the step's tokens, in the span
+  bool here;                // whether this group has a row
+  __device__ __forceinline__ void enter(const NormRopeParams& p, int s) {
+    span = s;
+    step = 0;
+    tok0 = s * p.span_tokens;
+    ntok = min(p.span_tokens, p.n_tokens - tok0);
+    steps = p.parts > 1 ? ntok * p.parts : (ntok + p.tokens_per_step - 1) / p.tokens_per_step;
+  }
+  __device__ __forceinline__ void place(const NormRopeParams& p, int group, int groups, int tl_group, int h_group) {
+    if (p.parts == 1) {
+      first = step * p.tokens_per_step;
+      n = min(p.tokens_per_step, ntok - first);
+      tl = first + tl_group;
+      h = h_group;
+      here = tl_group < n;
+    } else {
+      first = tl = p.div_parts(step);
+      n = 1;
+      h = (step - tl * p.parts) * groups + group;
+      here = h < p.H;
+    }
+    if (!here) { tl = first; h = 0; }
+  }
+  __device__ __forceinline__ const uint4* source(const NormRopeParams& p) const {
+    const int tok = tok0 + tl, b = p.div_l(tok), l = tok - b * p.L;
+    return reinterpret_cast<const uint4*>(p.x + b * p.stride_b + l * p.stride_l + h * p.stride_h);
+  }
+  // Vector offset of the row in a contiguous [tokens, H, D] tensor.
+  __device__ __forceinline__ size_t row(const NormRopeParams& p) const {
+    return ((size_t)(tok0 + tl) * p.H + h) * (p.D / 8);
+  }
+};
 
 __device__ __forceinline__ uint2 to_e4m3(const Vec8& y, float2 inv) {
   uint32_t code[4];
@@ -243,131 +289,123 @@ __device__ __forceinline__ uint2 to_e4m3(const Vec8& y, float2 inv) {
 // 1/scale; y / scale is computed as y * (1 / scale), a few fp32 steps from the quotient at most.
 __device__ __forceinline__ float inv_scale(float amax) { return 1.f / (amax * (1.f / 448.f)); }
 
-// Persistent blocks over chunks of rows, one row per group of G lanes and chunk.  A chunk is
-// tokens_per_block whole tokens, or (bf16 only) `groups` heads of one token.  While a chunk
-// is computed the next one's rows are in flight, and its angles are filled in before the
-// chunk's one barrier; that barrier also completes the tokens' maxima for e4m3.
-template <int G, int NP, int NM, bool E4M3>
+// Persistent blocks.  While a step is computed the next one's rows are in flight.  One
+// barrier per span completes its angles; e4m3 adds one per step, for the tokens' maxima.
+template <int G, int NP, int NM, bool E4M3, bool LAYER>
 __global__ void __launch_bounds__(E4M3 ? kMaxThreads : 256, (2 * NP + NM) > 6 ? 1 : E4M3 ? 1 : 2)
 norm_rope_kernel(const NormRopeParams p) {
   using S = Slots<G, NP, NM>;
   constexpr int N = S::kN;
   extern __shared__ __align__(16) float smem[];
-  const int table = p.tokens_per_block * p.n_freq;
-  float* amax3 = smem + 4 * table;                       // three buffers of one value per token (e4m3)
+  const int table = p.span_tokens * p.n_freq;
+  float* w = smem + 4 * table;                           // behind two buffers of cos and sin
+  float* amax3 = w + p.norm_dim * (p.b ? 2 : 1);         // three buffers of one value per token (e4m3)
   const int groups = blockDim.x / G;
   const int lane = threadIdx.x % G, group = threadIdx.x / G;
+  const int tl_group = p.div_h(group), h_group = group - tl_group * p.H;
   const S slots(p, lane);
-  const int parts = E4M3 ? 1 : (p.H + groups - 1) / groups;   // chunks of a token that fills more than one
-  // Chunk -> first token, tokens, this group's token in the chunk and head.
-  struct Place { int tok0, ntok, tl, h; bool here; };
-  auto place = [&](int ch) {
-    Place q;
-    if (parts == 1) {
-      q.tok0 = ch * p.tokens_per_block;
-      q.ntok = min(p.tokens_per_block, p.n_tokens - q.tok0);
-      q.tl = p.div_h(group);
-      q.h = group - q.tl * p.H;
-      q.here = q.tl < q.ntok;
-    } else {
-      q.tok0 = ch / parts;
-      q.ntok = 1;
-      q.tl = 0;
-      q.h = (ch - q.tok0 * parts) * groups + group;
-      q.here = q.h < p.H;
-    }
-    if (!q.here) q.tl = q.h = 0;                         // (reads the first token's angles, writes nothing)
-    return q;
-  };
+  griddep_launch_dependents();
+  griddep_wait();
   uint4 raw[N];
-  auto load = [&](const Place& q) {
-    const int tok = q.tok0 + q.tl, b = p.div_l(tok), l = tok - b * p.L;
-    const uint4* src = reinterpret_cast<const uint4*>(p.x + b * p.stride_b + l * p.stride_l + q.h * p.stride_h);
+  Walk q;
+  q.enter(p, blockIdx.x);
+  q.place(p, group, groups, tl_group, h_group);
+  auto load = [&]() {
+    const uint4* src = q.source(p);
 #pragma unroll
     for (int n = 0; n < N; ++n)
       raw[n] = q.here && slots.vec[n] >= 0 ? __ldg(src + slots.vec[n]) : make_uint4(0, 0, 0, 0);
   };
-  griddep_launch_dependents();
-  griddep_wait();
-  int ch = blockIdx.x;
-  Place q = place(ch);
-  load(q);
-  fill_angles(p, q.tok0, q.ntok, smem, smem + table);
+  load();
+  fill_params(p, w);
+  if (p.n_freq) fill_angles(p, q.tok0, q.ntok, smem, smem + table);
   if (E4M3)
-    for (int t = threadIdx.x; t < p.tokens_per_block; t += blockDim.x) amax3[t] = kAmaxFloor;
+    for (int t = threadIdx.x; t < p.tokens_per_step; t += blockDim.x) amax3[t] = kAmaxFloor;
   __syncthreads();
-  for (int it = 0, a3 = 0; ch < p.n_chunks; ch += gridDim.x, it ^= 1) {
-    const float* cs = smem + it * 2 * table;
+  int buf = 0, a3 = 0;
+  for (;;) {
+    Vec8 y[N];
+#pragma unroll
+    for (int n = 0; n < N; ++n) y[n] = unpack8(raw[n]);
+    const int tl = q.tl, first = q.first, n_now = q.n, tok_now = q.tok0 + q.first;
+    const bool here = q.here;
+    const size_t row = q.row(p);
+    const float* cs = smem + buf * 2 * table + tl * p.n_freq;
     const float* sn = cs + table;
-    float* amax = amax3 + a3 * p.tokens_per_block;
-    a3 = a3 == 2 ? 0 : a3 + 1;
-    float* amax_next = amax3 + a3 * p.tokens_per_block;
-    float mean, rstd;
-    row_stats<G, N>(p, raw, slots.vec, mean, rstd);
-    const size_t row = ((size_t)(q.tok0 + q.tl) * p.H + q.h) * (p.D / 8);   // of the output, in vectors
-    Vec8 y[E4M3 ? N : 1];
-    auto emit = [&](int n, const Vec8& z) {
-      if constexpr (E4M3) y[n] = z;
-      else if (q.here && slots.vec[n] >= 0) reinterpret_cast<uint4*>(p.out)[row + slots.vec[n]] = pack8(z);
-    };
-#pragma unroll
-    for (int n = 0; n < NP; ++n) {
-      Vec8 a = normed8(p, raw[2 * n], slots.vec[2 * n], mean, rstd);
-      Vec8 b = normed8(p, raw[2 * n + 1], slots.vec[2 * n + 1], mean, rstd);
-      if (p.n_freq && slots.vec[2 * n] >= 0)
-        rotate_pair(p, n * G + lane, a, b, cs + q.tl * p.n_freq, sn + q.tl * p.n_freq, 1.f);
-      emit(2 * n, a);
-      emit(2 * n + 1, b);
+    // The next step's rows.
+    const bool turn = q.step + 1 == q.steps;             // the span ends with this step
+    bool more = true;
+    if (!turn) {
+      ++q.step;
+    } else if (q.span + (int)gridDim.x < p.n_spans) {
+      q.enter(p, q.span + gridDim.x);
+    } else {
+      more = false;
     }
+    if (more) {
+      q.place(p, group, groups, tl_group, h_group);
+      load();
+    }
+    normalise<G, LAYER>(p, y, slots.vec);
 #pragma unroll
-    for (int n = 2 * NP; n < N; ++n) emit(n, normed8(p, raw[n], slots.vec[n], mean, rstd));
-
-    const Place now = q;
-    if (ch + (int)gridDim.x < p.n_chunks) {
-      q = place(ch + gridDim.x);
-      load(q);
-      float* tab = smem + (it ^ 1) * 2 * table;
-      fill_angles(p, q.tok0, q.ntok, tab, tab + table);
+    for (int n = 0; n < N; ++n) scale8<LAYER>(p, y[n], slots.vec[n], w);
+    if (p.n_freq)
+#pragma unroll
+      for (int n = 0; n < NP; ++n)
+        if (slots.vec[2 * n] >= 0) rotate_pair(p, n * G + lane, y[2 * n], y[2 * n + 1], cs, sn, 1.f);
+    if constexpr (!E4M3) {
+      if (here)
+#pragma unroll
+        for (int n = 0; n < N; ++n)
+          if (slots.vec[n] >= 0) reinterpret_cast<uint4*>(p.out)[row + slots.vec[n]] = pack8(y[n]);
+    }
+    if (turn && more) {
+      buf ^= 1;
+      if (p.n_freq) fill_angles(p, q.tok0, q.ntok, smem + buf * 2 * table, smem + buf * 2 * table + table);
     }
     if constexpr (E4M3) {
+      float* amax = amax3 + a3 * p.tokens_per_step;
+      a3 = a3 == 2 ? 0 : a3 + 1;
+      float* amax_next = amax3 + a3 * p.tokens_per_step;
       // The maximum does not depend on the order, and a NaN wins (also as an integer).
       float m = 0.f;
 #pragma unroll
       for (int n = 0; n < N; ++n)
 #pragma unroll
         for (int e = 0; e < 4; ++e) m = max_abs(max_abs(m, y[n].v[e].x), y[n].v[e].y);
-      if (!now.here) m = 0.f;
-      const bool one = p.H >= 32 / G && p.H % (32 / G) == 0;   // every row of the warp is of one token
+      if (!here) m = 0.f;
+      const bool one = p.H % (32 / G) == 0;              // every row of the warp is of one token
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1)
         if (o < G || one) m = max_abs(m, __shfl_xor_sync(0xffffffffu, m, o));
-      if ((one ? threadIdx.x % 32 : lane) == 0 && now.here)
-        atomicMax(reinterpret_cast<int*>(&amax[now.tl]), __float_as_int(m));
-      for (int t = threadIdx.x; t < p.tokens_per_block; t += blockDim.x) amax_next[t] = kAmaxFloor;
-    }
-    __syncthreads();
-    if constexpr (E4M3) {
-      if (threadIdx.x < now.ntok) p.scale[now.tok0 + threadIdx.x] = amax[threadIdx.x] / 448.f;
-      if (now.here) {
-        const float2 inv = both(inv_scale(amax[now.tl]));
+      if ((one ? threadIdx.x % 32 : lane) == 0 && here)
+        atomicMax(reinterpret_cast<int*>(&amax[tl - first]), __float_as_int(m));
+      for (int t = threadIdx.x; t < p.tokens_per_step; t += blockDim.x) amax_next[t] = kAmaxFloor;
+      __syncthreads();
+      if (threadIdx.x < n_now) p.scale[tok_now + threadIdx.x] = amax[threadIdx.x] / 448.f;
+      if (here) {
+        const float2 inv = both(inv_scale(amax[tl - first]));
         uint2* dst = reinterpret_cast<uint2*>(p.codes) + row;
 #pragma unroll
         for (int n = 0; n < N; ++n)
           if (slots.vec[n] >= 0) dst[slots.vec[n]] = to_e4m3(y[n], inv);
       }
+    } else {
+      if (turn && more) __syncthreads();
     }
+    if (!more) break;
   }
 }
 
 // e4m3 of tokens with more heads than a block holds: one block per token, the rows
 // computed twice (the second time from L2), first for the maximum.
-template <int G, int NP, int NM>
+template <int G, int NP, int NM, bool LAYER>
 __global__ void __launch_bounds__(kMaxThreads) norm_rope_wide_kernel(const NormRopeParams p) {
   using S = Slots<G, NP, NM>;
   constexpr int N = S::kN;
   extern __shared__ __align__(16) float smem[];
   __shared__ float amax;
-  float *cs = smem, *sn = smem + p.n_freq;
+  float *cs = smem, *sn = smem + p.n_freq, *w = sn + p.n_freq;
   const int groups = blockDim.x / G;
   const int lane = threadIdx.x % G, group = threadIdx.x / G;
   const S slots(p, lane);
@@ -375,7 +413,8 @@ __global__ void __launch_bounds__(kMaxThreads) norm_rope_wide_kernel(const NormR
   griddep_launch_dependents();
   griddep_wait();
   if (threadIdx.x == 0) amax = kAmaxFloor;
-  fill_angles(p, tok, 1, cs, sn);
+  fill_params(p, w);
+  if (p.n_freq) fill_angles(p, tok, 1, cs, sn);
   __syncthreads();
   float m = 0.f;
   for (int pass = 0; pass < 2; ++pass) {
@@ -383,15 +422,13 @@ __global__ void __launch_bounds__(kMaxThreads) norm_rope_wide_kernel(const NormR
       const int h = h0 + group;
       const bool here = h < p.H;
       const uint4* src = reinterpret_cast<const uint4*>(p.x + b * p.stride_b + l * p.stride_l + (here ? h : 0) * p.stride_h);
-      uint4 raw[N];
-#pragma unroll
-      for (int n = 0; n < N; ++n)
-        raw[n] = here && slots.vec[n] >= 0 ? __ldg(src + slots.vec[n]) : make_uint4(0, 0, 0, 0);
-      float mean, rstd;
-      row_stats<G, N>(p, raw, slots.vec, mean, rstd);
       Vec8 y[N];
 #pragma unroll
-      for (int n = 0; n < N; ++n) y[n] = normed8(p, raw[n], slots.vec[n], mean, rstd);
+      for (int n = 0; n < N; ++n)
+        y[n] = unpack8(here && slots.vec[n] >= 0 ? __ldg(src + slots.vec[n]) : make_uint4(0, 0, 0, 0));
+      normalise<G, LAYER>(p, y, slots.vec);
+#pragma unroll
+      for (int n = 0; n < N; ++n) scale8<LAYER>(p, y[n], slots.vec[n], w);
       if (p.n_freq)
 #pragma unroll
         for (int n = 0; n < NP; ++n)
@@ -400,9 +437,8 @@ __global__ void __launch_bounds__(kMaxThreads) norm_rope_wide_kernel(const NormR
       if (pass == 0) {
 #pragma unroll
         for (int n = 0; n < N; ++n)
-          if (slots.vec[n] >= 0)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) m = max_abs(max_abs(m, y[n].v[e].x), y[n].v[e].y);
+          for (int e = 0; e < 4; ++e) m = max_abs(max_abs(m, y[n].v[e].x), y[n].v[e].y);
       } else {
         const float2 inv = both(inv_scale(amax));
         uint2* dst = reinterpret_cast<uint2*>(p.codes) + ((size_t)tok * p.H + h) * (p.D / 8);
@@ -421,107 +457,96 @@ __global__ void __launch_bounds__(kMaxThreads) norm_rope_wide_kernel(const NormR
   }
 }
 
-// Gradient.  Persistent blocks: each walks its chunks of tokens, keeps the sums for dw
-// and db of its columns in registers, and leaves one partial row per block; a second
-// kernel adds the partial rows in block order, so the result does not depend on timing.
+// Gradient.  Each block keeps the sums for dw and db of its columns in registers over all its
+// steps and leaves one partial row; a second kernel adds the partial rows in block
+// order, so the result does not depend on timing.
 constexpr int kBwdThreads = 256;
 
-template <int G, int NP, int NM, bool BIAS>
+template <int G, int NP, int NM, bool LAYER>
 __global__ void __launch_bounds__(kBwdThreads, (2 * NP + NM) > 4 ? 1 : 2) norm_rope_bwd_kernel(const NormRopeParams p) {
   using S = Slots<G, NP, NM>;
   constexpr int N = S::kN, kGroups = kBwdThreads / G;
   extern __shared__ __align__(16) float smem[];
-  const int table = p.tokens_per_block * p.n_freq;
+  const int table = p.span_tokens * p.n_freq;
+  float* w = smem + 4 * table;
   const int lane = threadIdx.x % G, group = threadIdx.x / G;
+  const int tl_group = p.div_h(group), h_group = group - tl_group * p.H;
   const S slots(p, lane);
   griddep_launch_dependents();
   griddep_wait();
-  Vec8 dw[N], db[BIAS ? N : 1];
+  Vec8 dw[N], db[LAYER ? N : 1];
 #pragma unroll
   for (int n = 0; n < N; ++n)
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       dw[n].v[e] = both(0.f);
-      if (BIAS) db[n].v[e] = both(0.f);
+      if (LAYER) db[n].v[e] = both(0.f);
     }
-
-  const int n_chunks = (int)(((long long)p.n_tokens + p.tokens_per_block - 1) / p.tokens_per_block);
+  fill_params(p, w);
+  Walk q;
   int buf = 0;
-  for (int ch = blockIdx.x; ch < n_chunks; ch += gridDim.x, buf ^= 1) {
-    const int tok0 = ch * p.tokens_per_block;
-    const int ntok = min(p.tokens_per_block, p.n_tokens - tok0);
-    const int rows = ntok * p.H;
-    const int steps = (rows + kGroups - 1) / kGroups;
-    float* cs = smem + buf * 2 * table;         // two tables: the next chunk's may be filled
-    float* sn = cs + table;                     // while slower warps still read this one
-    for (int st = 0; st < steps; ++st) {
-      const int row = st * kGroups + group;
-      const bool here = row < rows;
-      const int tl = here ? p.div_h(row) : 0, h = here ? row - tl * p.H : 0;
+  for (int span = blockIdx.x; span < p.n_spans; span += gridDim.x, buf ^= 1) {
+    q.enter(p, span);
+    float* cs0 = smem + buf * 2 * table;
+    if (p.n_freq) fill_angles(p, q.tok0, q.ntok, cs0, cs0 + table);
+    __syncthreads();
+    for (; q.step < q.steps; ++q.step) {
+      q.place(p, group, kGroups, tl_group, h_group);
+      const size_t row = q.row(p);
+      const uint4* src = q.source(p);
+      const uint4* gsrc = reinterpret_cast<const uint4*>(p.dy) + row;
       uint4 raw[N], graw[N];
-      {
-        const int tok = tok0 + tl, b = p.div_l(tok), l = tok - b * p.L;
-        const uint4* src = reinterpret_cast<const uint4*>(p.x + b * p.stride_b + l * p.stride_l + h * p.stride_h);
-        const uint4* gsrc = reinterpret_cast<const uint4*>(p.dy + ((size_t)tok0 * p.H + row) * p.D);
 #pragma unroll
-        for (int n = 0; n < N; ++n) {
-          raw[n] = graw[n] = make_uint4(0, 0, 0, 0);
-          if (here && slots.vec[n] >= 0) {
-            if (slots.vec[n] * 8 < p.norm_dim) raw[n] = __ldg(src + slots.vec[n]);
-            graw[n] = __ldg(gsrc + slots.vec[n]);
-          }
+      for (int n = 0; n < N; ++n) {
+        raw[n] = graw[n] = make_uint4(0, 0, 0, 0);
+        if (q.here && slots.vec[n] >= 0) {
+          if (is_normed(p, slots.vec[n])) raw[n] = __ldg(src + slots.vec[n]);
+          graw[n] = __ldg(gsrc + slots.vec[n]);
         }
       }
-      if (st == 0) {
-        fill_angles(p, tok0, ntok, cs, sn);
-        __syncthreads();
-      }
-      float mean, rstd;
-      row_stats<G, N>(p, raw, slots.vec, mean, rstd);
-      if (!here) rstd = 0.f;                    // 1/sqrt(eps) may be infinite
-      Vec8 g[N];                                // dz, then dz w
+      Vec8 xh[N], g[N];                         // xhat; dz, then dz w
 #pragma unroll
-      for (int n = 0; n < N; ++n) g[n] = unpack8(graw[n]);
-      if (p.n_freq) {
+      for (int n = 0; n < N; ++n) {
+        xh[n] = unpack8(raw[n]);
+        g[n] = unpack8(graw[n]);
+      }
+      const float rstd = normalise<G, LAYER>(p, xh, slots.vec);
+      if (p.n_freq)
 #pragma unroll
         for (int n = 0; n < NP; ++n)
           if (slots.vec[2 * n] >= 0)
-            rotate_pair(p, n * G + lane, g[2 * n], g[2 * n + 1], cs + tl * p.n_freq, sn + tl * p.n_freq, -1.f);
-      }
-      const float2 r2 = both(rstd), nm = both(-mean);
+            rotate_pair(p, n * G + lane, g[2 * n], g[2 * n + 1], cs0 + q.tl * p.n_freq, cs0 + table + q.tl * p.n_freq,
+                        -1.f);
       float2 s1 = both(0.f), s2 = both(0.f);    // sums of g and of g xhat
-      if (p.norm != DSA_NORM_NONE) {
-#pragma unroll
-        for (int n = 0; n < N; ++n) {
-          if (slots.vec[n] < 0 || slots.vec[n] * 8 >= p.norm_dim) continue;
-          const Vec8 x = unpack8(raw[n]), w = load_param8(p.w, p.w_bf16, slots.vec[n] * 8);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float2 xh = fmul2(fadd2(x.v[e], nm), r2);
-            // a row past the end has dz = 0, so it adds nothing
-            dw[n].v[e] = ffma2(g[n].v[e], xh, dw[n].v[e]);
-            if (BIAS) db[n].v[e] = fadd2(db[n].v[e], g[n].v[e]);
-            g[n].v[e] = fmul2(g[n].v[e], w.v[e]);
-            s1 = fadd2(s1, g[n].v[e]);
-            s2 = ffma2(g[n].v[e], xh, s2);
-          }
-        }
-        const float inv_n = p.inv_norm_dim;
-        s2 = both(-group_sum<G>(s2.x + s2.y) * inv_n);
-        s1 = both(p.norm == DSA_NORM_LAYER ? -group_sum<G>(s1.x + s1.y) * inv_n : 0.f);
-      }
-      uint4* dst = reinterpret_cast<uint4*>(p.dx + ((size_t)tok0 * p.H + row) * p.D);
 #pragma unroll
       for (int n = 0; n < N; ++n) {
-        if (p.norm != DSA_NORM_NONE && slots.vec[n] * 8 < p.norm_dim) {
-          const Vec8 x = unpack8(raw[n]);
+        // a group without a row has dz = 0 but perhaps an infinite 1/std: it adds nothing
+        if (!q.here || !is_normed(p, slots.vec[n])) continue;
+        const Vec8 a = load_angles(w + slots.vec[n] * 8);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          dw[n].v[e] = ffma2(g[n].v[e], xh[n].v[e], dw[n].v[e]);
+          if (LAYER) db[n].v[e] = fadd2(db[n].v[e], g[n].v[e]);
+          g[n].v[e] = fmul2(g[n].v[e], a.v[e]);
+          if (LAYER) s1 = fadd2(s1, g[n].v[e]);
+          s2 = ffma2(g[n].v[e], xh[n].v[e], s2);
+        }
+      }
+      if (p.norm != DSA_NORM_NONE) {
+        s2 = both(-group_sum<G>(s2.x + s2.y) * p.inv_norm_dim);
+        if (LAYER) s1 = both(-group_sum<G>(s1.x + s1.y) * p.inv_norm_dim);
+      }
+      uint4* dst = reinterpret_cast<uint4*>(p.dx) + row;
+#pragma unroll
+      for (int n = 0; n < N; ++n) {
+        if (is_normed(p, slots.vec[n])) {
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const float2 xh = fmul2(fadd2(x.v[e], nm), r2);
-            g[n].v[e] = fmul2(r2, ffma2(xh, s2, fadd2(g[n].v[e], s1)));
+            const float2 t = ffma2(xh[n].v[e], s2, g[n].v[e]);
+            g[n].v[e] = fmul2(both(rstd), LAYER ? fadd2(t, s1) : t);
           }
         }
-        if (here && slots.vec[n] >= 0) dst[slots.vec[n]] = pack8(g[n]);
+        if (q.here && slots.vec[n] >= 0) dst[slots.vec[n]] = pack8(g[n]);
       }
     }
   }
@@ -531,19 +556,20 @@ __global__ void __launch_bounds__(kBwdThreads, (2 * NP + NM) > 4 ? 1 : 2) norm_r
   constexpr int kWarps = kBwdThreads / 32;
   const int warp = threadIdx.x / 32;
 #pragma unroll
-  for (int what = 0; what < (BIAS ? 2 : 1); ++what) {
+  for (int what = 0; what < (LAYER ? 2 : 1); ++what) {
+    if (what && !p.b) break;
     __syncthreads();
 #pragma unroll
     for (int n = 0; n < N; ++n) {
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        float2 t = what ? db[BIAS ? n : 0].v[e] : dw[n].v[e];
+        float2 t = what ? db[LAYER ? n : 0].v[e] : dw[n].v[e];
 #pragma unroll
         for (int o = 16; o >= G; o >>= 1) {
           t.x += __shfl_xor_sync(0xffffffffu, t.x, o);
           t.y += __shfl_xor_sync(0xffffffffu, t.y, o);
         }
-        if (threadIdx.x % 32 < G && slots.vec[n] >= 0 && slots.vec[n] * 8 < p.norm_dim)
+        if (threadIdx.x % 32 < G && is_normed(p, slots.vec[n]))
           *reinterpret_cast<float2*>(red + warp * p.norm_dim + slots.vec[n] * 8 + 2 * e) = t;
       }
     }
@@ -551,7 +577,7 @@ __global__ void __launch_bounds__(kBwdThreads, (2 * NP + NM) > 4 ? 1 : 2) norm_r
     for (int c = threadIdx.x; c < p.norm_dim; c += kBwdThreads) {
       float s = 0.f;
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) s += red[w * p.norm_dim + c];
+      for (int k = 0; k < kWarps; ++k) s += red[k * p.norm_dim + c];
       p.part[((size_t)what * gridDim.x + blockIdx.x) * p.norm_dim + c] = s;
     }
   }
@@ -601,15 +627,28 @@ cudaError_t by_width(const NormRopeParams& p, Fn&& f) {
   return cudaErrorInvalidValue;
 }
 
-// Tokens per block: what one step holds, spread over the SMs when there are few tokens,
-// with at most 16 KB of angles.
-int tokens_per_block(const NormRopeParams& p, int rows_per_step, int sms) {
-  long long t = rows_per_step / p.H;
-  const long long spread = ((long long)p.n_tokens + 2 * sms - 1) / (2 * sms);
+// Steps and spans for blocks of `groups` rows a step; returns the grid.
+//   step: as many whole tokens as a block holds, but with few tokens only as many as spread
+//         them over the SMs; or part of a token's heads when a block holds less than one;
+//   span: steps whose angles together give every thread of the block one to fill in, as
+//         long as each block still gets four spans (their work then evens out), and at
+//         most 16 KB of angles.
+unsigned plan_walk(NormRopeParams& p, int groups, int sms, int blocks) {
+  const long long n = p.n_tokens;
+  p.parts = (p.H + groups - 1) / groups;
+  p.div_parts = fast_div((uint32_t)p.parts);
+  long long t = groups / p.H;
+  const long long spread = (n + 2 * sms - 1) / (2 * sms);
   if (t > spread) t = spread;
   const long long table = p.n_freq ? 16384 / (8LL * p.n_freq) : t;
   if (t > table) t = table;
-  return t < 1 ? 1 : (int)t;
+  p.tokens_per_step = t < 1 ? 1 : (int)t;
+  long long k = p.n_freq ? 256 / ((long long)p.tokens_per_step * p.n_freq) : 8;
+  const long long even = n / (4LL * blocks * p.tokens_per_step);
+  if (k > even) k = even;
+  p.span_tokens = p.tokens_per_step * (k < 1 ? 1 : (int)k);
+  p.n_spans = (int)((n + p.span_tokens - 1) / p.span_tokens);
+  return (unsigned)(p.n_spans < blocks ? p.n_spans : blocks);
 }
 
 }  // namespace
@@ -618,20 +657,18 @@ cudaError_t launch_norm_rope(NormRopeParams p, int sms, cudaStream_t stream) {
   if (!p.n_freq) p.rot_start = 0;
   return by_width(p, [&](auto g, auto np, auto nm) {
     constexpr int G = decltype(g)::value, NP = decltype(np)::value, NM = decltype(nm)::value;
+    const bool layer = p.norm == DSA_NORM_LAYER;
+    const size_t params = (size_t)p.norm_dim * (p.b ? 2 : 1);
     if (p.codes && p.H > kMaxThreads / G)
-      return launch_pdl(norm_rope_wide_kernel<G, NP, NM>, dim3(p.n_tokens), dim3(kMaxThreads),
-                        (size_t)p.n_freq * 8, stream, p);
+      return launch_pdl(layer ? norm_rope_wide_kernel<G, NP, NM, true> : norm_rope_wide_kernel<G, NP, NM, false>,
+                        dim3(p.n_tokens), dim3(kMaxThreads), (2 * p.n_freq + params) * sizeof(float), stream, p);
     // Twice the threads where that lets a block hold all heads of a token (e4m3).
-    const int threads = p.codes && p.H > 256 / G ? kMaxThreads : 256, groups = threads / G;
-    p.tokens_per_block = tokens_per_block(p, groups, sms);
-    const long long chunks = p.H > groups ? (long long)p.n_tokens * ((p.H + groups - 1) / groups)
-                                          : ((long long)p.n_tokens + p.tokens_per_block - 1) / p.tokens_per_block;
-    if (chunks >= (1ll << 31) - sms * 8) return cudaErrorInvalidValue;
-    p.n_chunks = (int)chunks;
-    const long long most = (long long)sms * (threads == 256 ? kNormRopeBlocksPerSm : kNormRopeBlocksPerSm / 2);
-    const size_t smem = ((size_t)p.tokens_per_block * p.n_freq * 4 + 3 * p.tokens_per_block) * sizeof(float);
-    return launch_pdl(p.codes ? norm_rope_kernel<G, NP, NM, true> : norm_rope_kernel<G, NP, NM, false>,
-                      dim3((unsigned)(chunks < most ? chunks : most)), dim3(threads), smem, stream, p);
+    const int threads = p.codes && p.H > 256 / G ? kMaxThreads : 256;
+    const unsigned grid = plan_walk(p, threads / G, sms, sms * (threads == 256 ? kBlocksPerSm : kBlocksPerSm / 2));
+    const size_t smem = ((size_t)p.span_tokens * p.n_freq * 4 + params + 3 * p.tokens_per_step) * sizeof(float);
+    auto kern = p.codes ? (layer ? norm_rope_kernel<G, NP, NM, true, true> : norm_rope_kernel<G, NP, NM, true, false>)
+                        : (layer ? norm_rope_kernel<G, NP, NM, false, true> : norm_rope_kernel<G, NP, NM, false, false>);
+    return launch_pdl(kern, dim3(grid), dim3(threads), smem, stream, p);
   });
 }
 
@@ -642,14 +679,13 @@ cudaError_t launch_norm_rope_bwd(NormRopeParams p, int sms, cudaStream_t stream)
   int grid = 0;
   const cudaError_t e = by_width(p, [&](auto g, auto np, auto nm) {
     constexpr int G = decltype(g)::value, NP = decltype(np)::value, NM = decltype(nm)::value;
-    p.tokens_per_block = tokens_per_block(p, kBwdThreads / G, sms);
-    const long long chunks = ((long long)p.n_tokens + p.tokens_per_block - 1) / p.tokens_per_block;
-    const long long most = norm_rope_bwd_blocks(sms);
-    grid = (int)(chunks < most ? chunks : most);
-    size_t smem = (size_t)p.tokens_per_block * p.n_freq * 16;
-    const size_t red = (size_t)(kBwdThreads / 32) * p.norm_dim * 4;
+    grid = (int)plan_walk(p, kBwdThreads / G, sms, norm_rope_bwd_blocks(sms));
+    size_t smem = ((size_t)p.span_tokens * p.n_freq * 4 + p.norm_dim * (p.b ? 2 : 1)) * sizeof(float);
+    const size_t red = (size_t)(kBwdThreads / 32) * p.norm_dim * sizeof(float);
     if (red > smem) smem = red;
-    return launch_pdl(p.b ? norm_rope_bwd_kernel<G, NP, NM, true> : norm_rope_bwd_kernel<G, NP, NM, false>, dim3(grid), dim3(kBwdThreads), smem, stream, p);
+    return launch_pdl(p.norm == DSA_NORM_LAYER ? norm_rope_bwd_kernel<G, NP, NM, true>
+                                               : norm_rope_bwd_kernel<G, NP, NM, false>,
+                      dim3(grid), dim3(kBwdThreads), smem, stream, p);
   });
   if (e != cudaSuccess || p.norm == DSA_NORM_NONE) return e;
   return launch_pdl(norm_rope_sum_kernel, dim3((p.norm_dim + 31) / 32, p.b ? 2 : 1), dim3(256), 0, stream, p, grid);
