@@ -187,7 +187,7 @@ struct NormRopeParams {
   float* dw;              // [norm_dim]
   float* db;              // [norm_dim] (when b is given)
 };
-constexpr int kNormRopeBwdBlocksPerSm = 4;
+constexpr int kNormRopeBwdBlocksPerSm = 2;
 int norm_rope_bwd_blocks(int sms);   // most partial rows the gradient leaves
 cudaError_t launch_norm_rope(NormRopeParams p, int sms, cudaStream_t stream);
 cudaError_t launch_norm_rope_bwd(NormRopeParams p, int sms, cudaStream_t stream);

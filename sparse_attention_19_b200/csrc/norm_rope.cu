@@ -38,8 +38,10 @@ namespace dsa {
 
 namespace {
 
-constexpr int kMaxThreads = 512;
-constexpr int kBlocksPerSm = 4;                // blocks of 256 threads
+constexpr int kThreads = 256;
+// Blocks of an SM that the registers of the bf16 kernel are to allow: more rows in flight for
+// rows of few slots (the layer norm's second sum would spill there), fewer for rows of many.
+constexpr int resident(int slots, bool layer) { return slots > 6 ? 1 : slots > 4 || layer ? 2 : 3; }
 constexpr float kAmaxFloor = 1e-30f;           // an all-zero token keeps a positive scale
 
 struct Vec8 {
@@ -55,10 +57,10 @@ __device__ __forceinline__ float2 fmul2(float2 a, float2 b) {
 }
 __device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
 
-// max(m, |x|), NaN if either is.
-__device__ __forceinline__ float max_abs(float m, float x) {
+// max(|m|, |x|, |y|), NaN if one of them is.
+__device__ __forceinline__ float max_abs(float m, float x, float y) {
   float r;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(m), "f"(fabsf(x)));
+  asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(m), "f"(x), "f"(y));
   return r;
 }
 
@@ -101,25 +103,60 @@ __device__ __forceinline__ float group_sum(float x) {
 // Which vectors of a row a lane holds.  Slots 2n and 2n + 1 (n < NP) are the two members
 // of pair vector n * G + lane of the rotated range, the other slots its share of the rest.
 // Without a rotation the "range" is the row's first vectors, so that no slot is wasted.
-template <int G, int NP, int NM>
+// FULL rows fill every slot of every lane, the rotated range lies at one end of the row and
+// the norm covers all or none of it and of the rest: then nothing is checked per vector
+// (8K indexer queries to e4m3: 57 us with the checks, see the launch for the time without).
+template <int G, int NP, int NM, bool FULL>
 struct Slots {
   static constexpr int kN = 2 * NP + NM;
-  int vec[kN];               // -1: none
+  int v[FULL ? 1 : kN];      // -1: none
+  int pair0, main0;          // FULL: first pair and first other vector of this lane
+  bool pair_normed, main_normed;
+  int norm_dim;
   __device__ __forceinline__ Slots(const NormRopeParams& p, int lane) {
     const int nv = p.D / 8;
     const int V = p.n_freq ? p.n_freq / 8 : min(G * NP, nv / 2), rs = p.rot_start / 8;
+    norm_dim = p.norm_dim;
+    if constexpr (FULL) {
+      pair0 = rs + lane;
+      main0 = lane + (rs == 0 ? 2 * V : 0);
+      pair_normed = p.norm_dim > p.rot_start;
+      main_normed = p.norm_dim > (rs == 0 ? 16 * V : 0);
+    } else {
 #pragma unroll
-    for (int n = 0; n < NP; ++n) {
-      const int i = n * G + lane;
-      vec[2 * n] = i < V ? rs + i : -1;
-      vec[2 * n + 1] = i < V ? rs + V + i : -1;
-    }
+      for (int n = 0; n < NP; ++n) {
+        const int i = n * G + lane;
+        v[2 * n] = i < V ? rs + i : -1;
+        v[2 * n + 1] = i < V ? rs + V + i : -1;
+      }
 #pragma unroll
-    for (int n = 0; n < NM; ++n) {
-      int i = n * G + lane;
-      if (i >= rs) i += 2 * V;
-      vec[2 * NP + n] = i < nv ? i : -1;
+      for (int n = 0; n < NM; ++n) {
+        int i = n * G + lane;
+        if (i >= rs) i += 2 * V;
+        v[2 * NP + n] = i < nv ? i : -1;
+      }
     }
+  }
+  static bool full(const NormRopeParams& p) {
+    const int nv = p.D / 8, V = p.n_freq ? p.n_freq / 8 : (G * NP < nv / 2 ? G * NP : nv / 2);
+    const int rs = p.rot_start / 8, rest = nv - 2 * V;
+    if (V != G * NP || rest != G * NM || (rs != 0 && rs != rest)) return false;
+    return p.norm_dim == 0 || p.norm_dim == p.D || (rest > 0 && p.norm_dim == 8 * (rs == 0 ? 2 * V : rest));
+  }
+  __device__ __forceinline__ int vec(int n) const {
+    if constexpr (FULL) return n >= 2 * NP ? main0 + (n - 2 * NP) * G : pair0 + (n / 2 + (n % 2) * NP) * G;
+    else return v[n];
+  }
+  __device__ __forceinline__ bool has(int n) const { return FULL || vec(n) >= 0; }
+  // Whether the vector is normalised (norm_dim is 0 without a norm).
+  __device__ __forceinline__ bool normed(int n) const {
+    if constexpr (FULL) return n >= 2 * NP ? main_normed : pair_normed;
+    else return (unsigned)(vec(n) * 8) < (unsigned)norm_dim;
+  }
+  // Vector n of a row; a group without a row was given an address that can be read.
+  __device__ __forceinline__ uint4 load(const uint4* src, int n, bool here) const {
+    if constexpr (FULL) return __ldg(src + vec(n));
+    else return here && has(n) ? __ldg(src + vec(n)) : make_uint4(0, 0, 0, 0);
   }
 };
 
@@ -177,40 +214,35 @@ __device__ __forceinline__ void rotate_pair(const NormRopeParams& p, int i, Vec8
   }
 }
 
-// Whether a vector is normalised (norm_dim is 0 without a norm; no vector: -1).
-__device__ __forceinline__ bool is_normed(const NormRopeParams& p, int vec) {
-  return (unsigned)(vec * 8) < (unsigned)p.norm_dim;
-}
-
 // x -> xhat = (x - mean) / std over the norm_dim leading columns of a row held by G lanes;
 // returns 1/std.  Columns behind them stay as they are.
-template <int G, bool LAYER, int N>
-__device__ __forceinline__ float normalise(const NormRopeParams& p, Vec8 (&x)[N], const int (&vec)[N]) {
+template <int G, bool LAYER, int N, typename S>
+__device__ __forceinline__ float normalise(const NormRopeParams& p, Vec8 (&x)[N], const S& slots) {
   if (p.norm == DSA_NORM_NONE) return 1.f;
   if constexpr (LAYER) {
     float2 s = both(0.f);
 #pragma unroll
     for (int n = 0; n < N; ++n)
-      if (is_normed(p, vec[n]))
+      if (slots.normed(n))
 #pragma unroll
         for (int e = 0; e < 4; ++e) s = fadd2(s, x[n].v[e]);
     const float2 nm = both(-group_sum<G>(s.x + s.y) * p.inv_norm_dim);
 #pragma unroll
     for (int n = 0; n < N; ++n)
-      if (is_normed(p, vec[n]))
+      if (slots.normed(n))
 #pragma unroll
         for (int e = 0; e < 4; ++e) x[n].v[e] = fadd2(x[n].v[e], nm);
   }
   float2 q = both(0.f);
 #pragma unroll
   for (int n = 0; n < N; ++n)
-    if (is_normed(p, vec[n]))
+    if (slots.normed(n))
 #pragma unroll
       for (int e = 0; e < 4; ++e) q = ffma2(x[n].v[e], x[n].v[e], q);
   const float rstd = rsqrtf(group_sum<G>(q.x + q.y) * p.inv_norm_dim + p.eps);
 #pragma unroll
   for (int n = 0; n < N; ++n)
-    if (is_normed(p, vec[n]))
+    if (slots.normed(n))
 #pragma unroll
       for (int e = 0; e < 4; ++e) x[n].v[e] = fmul2(x[n].v[e], both(rstd));
   return rstd;
@@ -225,9 +257,10 @@ __device__ __forceinline__ void fill_params(const NormRopeParams& p, float* w) {
 }
 
 // z = xhat w + b.
-template <bool LAYER>
-__device__ __forceinline__ void scale8(const NormRopeParams& p, Vec8& z, int vec, const float* w) {
-  if (!is_normed(p, vec)) return;
+template <bool LAYER, typename S>
+__device__ __forceinline__ void scale8(const NormRopeParams& p, Vec8& z, const S& slots, int n, const float* w) {
+  if (!slots.normed(n)) return;
+  const int vec = slots.vec(n);
   const Vec8 a = load_angles(w + vec * 8);
   if (LAYER && p.b) {
     const Vec8 b = load_angles(w + p.norm_dim + vec * 8);
@@ -241,12 +274,21 @@ __device__ __forceinline__ void scale8(const NormRopeParams& p, Vec8& z, int vec
 
 // Steps of a block: spans blockIdx.x, blockIdx.x + gridDim.x, ... of span_tokens tokens, each in
 // steps of one row per group of lanes: tokens_per_step whole tokens, or part of a token's heads.
+struct Row {
+  int tok, h;
+  bool here;                // whether the group has a row in this step (else: the step's first token)
+  __device__ __forceinline__ const uint4* source(const NormRopeParams& p) const {
+    const int b = p.div_l(tok), l = tok - b * p.L;
+    return reinterpret_cast<const uint4*>(p.x + b * p.stride_b + l * p.stride_l + h * p.stride_h);
+  }
+  // Vector offset in a contiguous [tokens, H, D] tensor.
+  __device__ __forceinline__ size_t offset(const NormRopeParams& p) const {
+    return ((size_t)tok * p.H + h) * (p.D / 8);
+  }
+};
 struct Walk {
   int span, step, steps;    // steps: of this span
   int tok0, ntok;           // of the span
-  int tl, h;                // this group's row: token in the span and head
-  int first, n;             // the step's tokens, in the span
-  bool here;                // whether this group has a row
   __device__ __forceinline__ void enter(const NormRopeParams& p, int s) {
     span = s;
     step = 0;
@@ -254,28 +296,24 @@ struct Walk {
     ntok = min(p.span_tokens, p.n_tokens - tok0);
     steps = p.parts > 1 ? ntok * p.parts : (ntok + p.tokens_per_step - 1) / p.tokens_per_step;
   }
-  __device__ __forceinline__ void place(const NormRopeParams& p, int group, int groups, int tl_group, int h_group) {
+  // Tokens of a step of whole tokens: the first (in the span) and how many.
+  __device__ __forceinline__ int first(const NormRopeParams& p) const { return step * p.tokens_per_step; }
+  __device__ __forceinline__ int count(const NormRopeParams& p) const { return min(p.tokens_per_step, ntok - first(p)); }
+  // The row of the group that holds head h_in of the step's token tl_in (whole tokens), or
+  // the group-th of `groups` heads (part of a token).
+  __device__ __forceinline__ Row row(const NormRopeParams& p, int tl_in, int h_in, int group, int groups) const {
+    Row r;
     if (p.parts == 1) {
-      first = step * p.tokens_per_step;
-      n = min(p.tokens_per_step, ntok - first);
-      tl = first + tl_group;
-      h = h_group;
-      here = tl_group < n;
+      r.here = tl_in < count(p);
+      r.tok = tok0 + first(p) + (r.here ? tl_in : 0);
+      r.h = r.here ? h_in : 0;
     } else {
-      first = tl = p.div_parts(step);
-      n = 1;
-      h = (step - tl * p.parts) * groups + group;
-      here = h < p.H;
+      const int tl = p.div_parts(step), h = (step - tl * p.parts) * groups + group;
+      r.here = h < p.H;
+      r.tok = tok0 + tl;
+      r.h = r.here ? h : 0;
     }
-    if (!here) { tl = first; h = 0; }
-  }
-  __device__ __forceinline__ const uint4* source(const NormRopeParams& p) const {
-    const int tok = tok0 + tl, b = p.div_l(tok), l = tok - b * p.L;
-    return reinterpret_cast<const uint4*>(p.x + b * p.stride_b + l * p.stride_l + h * p.stride_h);
-  }
-  // Vector offset of the row in a contiguous [tokens, H, D] tensor.
-  __device__ __forceinline__ size_t row(const NormRopeParams& p) const {
-    return ((size_t)(tok0 + tl) * p.H + h) * (p.D / 8);
+    return r;
   }
 };
 
@@ -289,18 +327,15 @@ __device__ __forceinline__ uint2 to_e4m3(const Vec8& y, float2 inv) {
 // 1/scale; y / scale is computed as y * (1 / scale), a few fp32 steps from the quotient at most.
 __device__ __forceinline__ float inv_scale(float amax) { return 1.f / (amax * (1.f / 448.f)); }
 
-// Persistent blocks.  While a step is computed the next one's rows are in flight.  One
-// barrier per span completes its angles; e4m3 adds one per step, for the tokens' maxima.
-template <int G, int NP, int NM, bool E4M3, bool LAYER>
-__global__ void __launch_bounds__(E4M3 ? kMaxThreads : 256, (2 * NP + NM) > 6 ? 1 : E4M3 ? 1 : 2)
-norm_rope_kernel(const NormRopeParams p) {
-  using S = Slots<G, NP, NM>;
-  constexpr int N = S::kN;
+// bf16 output.  Persistent blocks; while a step is computed the next one's rows are in
+// flight, and one barrier per span completes its angles.
+template <int G, int NP, int NM, bool FULL, bool LAYER>
+__global__ void __launch_bounds__(kThreads, resident(2 * NP + NM, LAYER)) norm_rope_kernel(const NormRopeParams p) {
+  using S = Slots<G, NP, NM, FULL>;
+  constexpr int N = S::kN, kGroups = kThreads / G;
   extern __shared__ __align__(16) float smem[];
   const int table = p.span_tokens * p.n_freq;
   float* w = smem + 4 * table;                           // behind two buffers of cos and sin
-  float* amax3 = w + p.norm_dim * (p.b ? 2 : 1);         // three buffers of one value per token (e4m3)
-  const int groups = blockDim.x / G;
   const int lane = threadIdx.x % G, group = threadIdx.x / G;
   const int tl_group = p.div_h(group), h_group = group - tl_group * p.H;
   const S slots(p, lane);
@@ -308,31 +343,26 @@ norm_rope_kernel(const NormRopeParams p) {
   griddep_wait();
   uint4 raw[N];
   Walk q;
+  Row r;
   q.enter(p, blockIdx.x);
-  q.place(p, group, groups, tl_group, h_group);
   auto load = [&]() {
-    const uint4* src = q.source(p);
+    r = q.row(p, tl_group, h_group, group, kGroups);
+    const uint4* src = r.source(p);
 #pragma unroll
     for (int n = 0; n < N; ++n)
-      raw[n] = q.here && slots.vec[n] >= 0 ? __ldg(src + slots.vec[n]) : make_uint4(0, 0, 0, 0);
+      raw[n] = slots.load(src, n, r.here);
   };
   load();
   fill_params(p, w);
   if (p.n_freq) fill_angles(p, q.tok0, q.ntok, smem, smem + table);
-  if (E4M3)
-    for (int t = threadIdx.x; t < p.tokens_per_step; t += blockDim.x) amax3[t] = kAmaxFloor;
   __syncthreads();
-  int buf = 0, a3 = 0;
-  for (;;) {
+  for (int buf = 0;;) {
     Vec8 y[N];
 #pragma unroll
     for (int n = 0; n < N; ++n) y[n] = unpack8(raw[n]);
-    const int tl = q.tl, first = q.first, n_now = q.n, tok_now = q.tok0 + q.first;
-    const bool here = q.here;
-    const size_t row = q.row(p);
-    const float* cs = smem + buf * 2 * table + tl * p.n_freq;
-    const float* sn = cs + table;
-    // The next step's rows.
+    const bool here = r.here;
+    uint4* dst = reinterpret_cast<uint4*>(p.out) + r.offset(p);
+    const float* cs = smem + buf * 2 * table + (r.tok - q.tok0) * p.n_freq;
     const bool turn = q.step + 1 == q.steps;             // the span ends with this step
     bool more = true;
     if (!turn) {
@@ -342,66 +372,127 @@ norm_rope_kernel(const NormRopeParams p) {
     } else {
       more = false;
     }
-    if (more) {
-      q.place(p, group, groups, tl_group, h_group);
-      load();
-    }
-    normalise<G, LAYER>(p, y, slots.vec);
+    if (more) load();
+    normalise<G, LAYER>(p, y, slots);
 #pragma unroll
-    for (int n = 0; n < N; ++n) scale8<LAYER>(p, y[n], slots.vec[n], w);
+    for (int n = 0; n < N; ++n) scale8<LAYER>(p, y[n], slots, n, w);
     if (p.n_freq)
 #pragma unroll
       for (int n = 0; n < NP; ++n)
-        if (slots.vec[2 * n] >= 0) rotate_pair(p, n * G + lane, y[2 * n], y[2 * n + 1], cs, sn, 1.f);
-    if constexpr (!E4M3) {
-      if (here)
+        if (slots.has(2 * n)) rotate_pair(p, n * G + lane, y[2 * n], y[2 * n + 1], cs, cs + table, 1.f);
+    if (here)
 #pragma unroll
-        for (int n = 0; n < N; ++n)
-          if (slots.vec[n] >= 0) reinterpret_cast<uint4*>(p.out)[row + slots.vec[n]] = pack8(y[n]);
-    }
-    if (turn && more) {
+      for (int n = 0; n < N; ++n)
+        if (slots.has(n)) dst[slots.vec(n)] = pack8(y[n]);
+    if (!more) break;
+    if (turn) {
       buf ^= 1;
       if (p.n_freq) fill_angles(p, q.tok0, q.ntok, smem + buf * 2 * table, smem + buf * 2 * table + table);
+      __syncthreads();
     }
-    if constexpr (E4M3) {
-      float* amax = amax3 + a3 * p.tokens_per_step;
-      a3 = a3 == 2 ? 0 : a3 + 1;
-      float* amax_next = amax3 + a3 * p.tokens_per_step;
-      // The maximum does not depend on the order, and a NaN wins (also as an integer).
-      float m = 0.f;
+  }
+}
+
+// e4m3 output.  A step holds whole tokens, R rows per group of lanes in registers (so that the
+// weights are read once for R rows, and the one barrier a step needs for its tokens'
+// maxima serves R times the rows).
+template <int G, int NP, int NM, bool FULL, int R, bool LAYER>
+__global__ void __launch_bounds__(kThreads, 2 * NP + NM > 6 ? 1 : R > 1 || 2 * NP + NM > 4 ? 2 : LAYER ? 3 : 4) norm_rope_e4m3_kernel(const NormRopeParams p) {
+  using S = Slots<G, NP, NM, FULL>;
+  constexpr int N = S::kN, kGroups = kThreads / G;
+  extern __shared__ __align__(16) float smem[];
+  const int table = p.span_tokens * p.n_freq;
+  float* w = smem + 4 * table;                           // behind two buffers of cos and sin
+  float* amax3 = w + p.norm_dim * (p.b ? 2 : 1);         // three buffers of one value per token
+  const int lane = threadIdx.x % G, group = threadIdx.x / G;
+  int tl_group[R], h_group[R];
+#pragma unroll
+  for (int i = 0; i < R; ++i) {
+    tl_group[i] = p.div_h(i * kGroups + group);
+    h_group[i] = i * kGroups + group - tl_group[i] * p.H;
+  }
+  const S slots(p, lane);
+  griddep_launch_dependents();
+  griddep_wait();
+  fill_params(p, w);
+  for (int t = threadIdx.x; t < p.tokens_per_step; t += kThreads) amax3[t] = kAmaxFloor;
+  int buf = 0, a3 = 0;
+  Walk q;
+  for (int span = blockIdx.x; span < p.n_spans; span += gridDim.x, buf ^= 1) {
+    q.enter(p, span);
+    const float* cs0 = smem + buf * 2 * table;
+    for (; q.step < q.steps; ++q.step) {
+      Row r[R];
+      uint4 raw[R][N];
+#pragma unroll
+      for (int i = 0; i < R; ++i) {
+        r[i] = q.row(p, tl_group[i], h_group[i], 0, 0);
+        const uint4* src = r[i].source(p);
+#pragma unroll
+        for (int n = 0; n < N; ++n)
+          raw[i][n] = slots.load(src, n, r[i].here);
+      }
+      if (q.step == 0) {
+        if (p.n_freq) fill_angles(p, q.tok0, q.ntok, smem + buf * 2 * table, smem + buf * 2 * table + table);
+        __syncthreads();
+      }
+      Vec8 y[R][N];
+#pragma unroll
+      for (int i = 0; i < R; ++i) {
+#pragma unroll
+        for (int n = 0; n < N; ++n) y[i][n] = unpack8(raw[i][n]);
+        normalise<G, LAYER>(p, y[i], slots);
+      }
 #pragma unroll
       for (int n = 0; n < N; ++n)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) m = max_abs(max_abs(m, y[n].v[e].x), y[n].v[e].y);
-      if (!here) m = 0.f;
-      const bool one = p.H % (32 / G) == 0;              // every row of the warp is of one token
+        for (int i = 0; i < R; ++i) scale8<LAYER>(p, y[i][n], slots, n, w);
+      float* amax = amax3 + a3 * p.tokens_per_step;
+      a3 = a3 == 2 ? 0 : a3 + 1;
+      float* amax_next = amax3 + a3 * p.tokens_per_step;
+      const int first = q.tok0 + q.first(p);
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1)
-        if (o < G || one) m = max_abs(m, __shfl_xor_sync(0xffffffffu, m, o));
-      if ((one ? threadIdx.x % 32 : lane) == 0 && here)
-        atomicMax(reinterpret_cast<int*>(&amax[tl - first]), __float_as_int(m));
-      for (int t = threadIdx.x; t < p.tokens_per_step; t += blockDim.x) amax_next[t] = kAmaxFloor;
-      __syncthreads();
-      if (threadIdx.x < n_now) p.scale[tok_now + threadIdx.x] = amax[threadIdx.x] / 448.f;
-      if (here) {
-        const float2 inv = both(inv_scale(amax[tl - first]));
-        uint2* dst = reinterpret_cast<uint2*>(p.codes) + row;
+      for (int i = 0; i < R; ++i) {
+        const float* cs = cs0 + (r[i].tok - q.tok0) * p.n_freq;
+        if (p.n_freq)
+#pragma unroll
+          for (int n = 0; n < NP; ++n)
+            if (slots.has(2 * n)) rotate_pair(p, n * G + lane, y[i][2 * n], y[i][2 * n + 1], cs, cs + table, 1.f);
+        // The maximum does not depend on the order, and a NaN wins (also as an integer).
+        float m = 0.f;
 #pragma unroll
         for (int n = 0; n < N; ++n)
-          if (slots.vec[n] >= 0) dst[slots.vec[n]] = to_e4m3(y[n], inv);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) m = max_abs(m, y[i][n].v[e].x, y[i][n].v[e].y);
+        if (!r[i].here) m = 0.f;
+        const bool one = p.H % (32 / G) == 0;            // every row of the warp is of one token
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1)
+          if (o < G || one) m = max_abs(m, __shfl_xor_sync(0xffffffffu, m, o), 0.f);
+        if ((one ? threadIdx.x % 32 : lane) == 0 && r[i].here)
+          atomicMax(reinterpret_cast<int*>(&amax[r[i].tok - first]), __float_as_int(m));
       }
-    } else {
-      if (turn && more) __syncthreads();
+      for (int t = threadIdx.x; t < p.tokens_per_step; t += kThreads) amax_next[t] = kAmaxFloor;
+      __syncthreads();
+      if (threadIdx.x < q.count(p)) p.scale[first + threadIdx.x] = amax[threadIdx.x] / 448.f;
+#pragma unroll
+      for (int i = 0; i < R; ++i) {
+        if (!r[i].here) continue;
+        const float2 inv = both(inv_scale(amax[r[i].tok - first]));
+        uint2* dst = reinterpret_cast<uint2*>(p.codes) + r[i].offset(p);
+#pragma unroll
+        for (int n = 0; n < N; ++n)
+          if (slots.has(n)) dst[slots.vec(n)] = to_e4m3(y[i][n], inv);
+      }
     }
-    if (!more) break;
   }
 }
 
 // e4m3 of tokens with more heads than a block holds: one block per token, the rows
 // computed twice (the second time from L2), first for the maximum.
 template <int G, int NP, int NM, bool LAYER>
-__global__ void __launch_bounds__(kMaxThreads) norm_rope_wide_kernel(const NormRopeParams p) {
-  using S = Slots<G, NP, NM>;
+__global__ void __launch_bounds__(kThreads) norm_rope_wide_kernel(const NormRopeParams p) {
+  using S = Slots<G, NP, NM, false>;
   constexpr int N = S::kN;
   extern __shared__ __align__(16) float smem[];
   __shared__ float amax;
@@ -425,31 +516,31 @@ __global__ void __launch_bounds__(kMaxThreads) norm_rope_wide_kernel(const NormR
       Vec8 y[N];
 #pragma unroll
       for (int n = 0; n < N; ++n)
-        y[n] = unpack8(here && slots.vec[n] >= 0 ? __ldg(src + slots.vec[n]) : make_uint4(0, 0, 0, 0));
-      normalise<G, LAYER>(p, y, slots.vec);
+        y[n] = unpack8(slots.load(src, n, here));
+      normalise<G, LAYER>(p, y, slots);
 #pragma unroll
-      for (int n = 0; n < N; ++n) scale8<LAYER>(p, y[n], slots.vec[n], w);
+      for (int n = 0; n < N; ++n) scale8<LAYER>(p, y[n], slots, n, w);
       if (p.n_freq)
 #pragma unroll
         for (int n = 0; n < NP; ++n)
-          if (slots.vec[2 * n] >= 0) rotate_pair(p, n * G + lane, y[2 * n], y[2 * n + 1], cs, sn, 1.f);
+          if (slots.has(2 * n)) rotate_pair(p, n * G + lane, y[2 * n], y[2 * n + 1], cs, sn, 1.f);
       if (!here) continue;
       if (pass == 0) {
 #pragma unroll
         for (int n = 0; n < N; ++n)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) m = max_abs(max_abs(m, y[n].v[e].x), y[n].v[e].y);
+          for (int e = 0; e < 4; ++e) m = max_abs(m, y[n].v[e].x, y[n].v[e].y);
       } else {
         const float2 inv = both(inv_scale(amax));
         uint2* dst = reinterpret_cast<uint2*>(p.codes) + ((size_t)tok * p.H + h) * (p.D / 8);
 #pragma unroll
         for (int n = 0; n < N; ++n)
-          if (slots.vec[n] >= 0) dst[slots.vec[n]] = to_e4m3(y[n], inv);
+          if (slots.has(n)) dst[slots.vec(n)] = to_e4m3(y[n], inv);
       }
     }
     if (pass == 0) {
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) m = max_abs(m, __shfl_xor_sync(0xffffffffu, m, o));
+      for (int o = 16; o > 0; o >>= 1) m = max_abs(m, __shfl_xor_sync(0xffffffffu, m, o), 0.f);
       if (threadIdx.x % 32 == 0) atomicMax(reinterpret_cast<int*>(&amax), __float_as_int(m));
       __syncthreads();
       if (threadIdx.x == 0) p.scale[tok] = amax / 448.f;
@@ -460,12 +551,10 @@ __global__ void __launch_bounds__(kMaxThreads) norm_rope_wide_kernel(const NormR
 // Gradient.  Each block keeps the sums for dw and db of its columns in registers over all its
 // steps and leaves one partial row; a second kernel adds the partial rows in block
 // order, so the result does not depend on timing.
-constexpr int kBwdThreads = 256;
-
-template <int G, int NP, int NM, bool LAYER>
-__global__ void __launch_bounds__(kBwdThreads, (2 * NP + NM) > 4 ? 1 : 2) norm_rope_bwd_kernel(const NormRopeParams p) {
-  using S = Slots<G, NP, NM>;
-  constexpr int N = S::kN, kGroups = kBwdThreads / G;
+template <int G, int NP, int NM, bool FULL, bool LAYER>
+__global__ void __launch_bounds__(kThreads, (2 * NP + NM) > 4 ? 1 : 2) norm_rope_bwd_kernel(const NormRopeParams p) {
+  using S = Slots<G, NP, NM, FULL>;
+  constexpr int N = S::kN, kGroups = kThreads / G;
   extern __shared__ __align__(16) float smem[];
   const int table = p.span_tokens * p.n_freq;
   float* w = smem + 4 * table;
@@ -491,18 +580,16 @@ __global__ void __launch_bounds__(kBwdThreads, (2 * NP + NM) > 4 ? 1 : 2) norm_r
     if (p.n_freq) fill_angles(p, q.tok0, q.ntok, cs0, cs0 + table);
     __syncthreads();
     for (; q.step < q.steps; ++q.step) {
-      q.place(p, group, kGroups, tl_group, h_group);
-      const size_t row = q.row(p);
-      const uint4* src = q.source(p);
+      const Row r = q.row(p, tl_group, h_group, group, kGroups);
+      const size_t row = r.offset(p);
+      const uint4* src = r.source(p);
       const uint4* gsrc = reinterpret_cast<const uint4*>(p.dy) + row;
       uint4 raw[N], graw[N];
 #pragma unroll
       for (int n = 0; n < N; ++n) {
-        raw[n] = graw[n] = make_uint4(0, 0, 0, 0);
-        if (q.here && slots.vec[n] >= 0) {
-          if (is_normed(p, slots.vec[n])) raw[n] = __ldg(src + slots.vec[n]);
-          graw[n] = __ldg(gsrc + slots.vec[n]);
-        }
+        raw[n] = make_uint4(0, 0, 0, 0);
+        if (slots.normed(n)) raw[n] = slots.load(src, n, r.here);
+        graw[n] = slots.load(gsrc, n, r.here);
       }
       Vec8 xh[N], g[N];                         // xhat; dz, then dz w
 #pragma unroll
@@ -510,19 +597,18 @@ __global__ void __launch_bounds__(kBwdThreads, (2 * NP + NM) > 4 ? 1 : 2) norm_r
         xh[n] = unpack8(raw[n]);
         g[n] = unpack8(graw[n]);
       }
-      const float rstd = normalise<G, LAYER>(p, xh, slots.vec);
+      const float rstd = normalise<G, LAYER>(p, xh, slots);
       if (p.n_freq)
 #pragma unroll
         for (int n = 0; n < NP; ++n)
-          if (slots.vec[2 * n] >= 0)
-            rotate_pair(p, n * G + lane, g[2 * n], g[2 * n + 1], cs0 + q.tl * p.n_freq, cs0 + table + q.tl * p.n_freq,
-                        -1.f);
+          if (slots.has(2 * n))
+            rotate_pair(p, n * G + lane, g[2 * n], g[2 * n + 1], cs0 + (r.tok - q.tok0) * p.n_freq,
+                        cs0 + table + (r.tok - q.tok0) * p.n_freq, -1.f);
       float2 s1 = both(0.f), s2 = both(0.f);    // sums of g and of g xhat
 #pragma unroll
       for (int n = 0; n < N; ++n) {
-        // a group without a row has dz = 0 but perhaps an infinite 1/std: it adds nothing
-        if (!q.here || !is_normed(p, slots.vec[n])) continue;
-        const Vec8 a = load_angles(w + slots.vec[n] * 8);
+        if (!r.here || !slots.normed(n)) continue;   // a group without a row adds nothing
+        const Vec8 a = load_angles(w + slots.vec(n) * 8);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           dw[n].v[e] = ffma2(g[n].v[e], xh[n].v[e], dw[n].v[e]);
@@ -539,21 +625,21 @@ __global__ void __launch_bounds__(kBwdThreads, (2 * NP + NM) > 4 ? 1 : 2) norm_r
       uint4* dst = reinterpret_cast<uint4*>(p.dx) + row;
 #pragma unroll
       for (int n = 0; n < N; ++n) {
-        if (is_normed(p, slots.vec[n])) {
+        if (slots.normed(n)) {
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const float2 t = ffma2(xh[n].v[e], s2, g[n].v[e]);
             g[n].v[e] = fmul2(both(rstd), LAYER ? fadd2(t, s1) : t);
           }
         }
-        if (q.here && slots.vec[n] >= 0) dst[slots.vec[n]] = pack8(g[n]);
+        if (r.here && slots.has(n)) dst[slots.vec(n)] = pack8(g[n]);
       }
     }
   }
   if (p.norm == DSA_NORM_NONE) return;
   // Sum the rows of each warp (exchange) and then the warps (shared memory), in a fixed order.
   float* red = smem;                            // [warps][norm_dim]
-  constexpr int kWarps = kBwdThreads / 32;
+  constexpr int kWarps = kThreads / 32;
   const int warp = threadIdx.x / 32;
 #pragma unroll
   for (int what = 0; what < (LAYER ? 2 : 1); ++what) {
@@ -569,12 +655,12 @@ __global__ void __launch_bounds__(kBwdThreads, (2 * NP + NM) > 4 ? 1 : 2) norm_r
           t.x += __shfl_xor_sync(0xffffffffu, t.x, o);
           t.y += __shfl_xor_sync(0xffffffffu, t.y, o);
         }
-        if (threadIdx.x % 32 < G && is_normed(p, slots.vec[n]))
-          *reinterpret_cast<float2*>(red + warp * p.norm_dim + slots.vec[n] * 8 + 2 * e) = t;
+        if (threadIdx.x % 32 < G && slots.normed(n))
+          *reinterpret_cast<float2*>(red + warp * p.norm_dim + slots.vec(n) * 8 + 2 * e) = t;
       }
     }
     __syncthreads();
-    for (int c = threadIdx.x; c < p.norm_dim; c += kBwdThreads) {
+    for (int c = threadIdx.x; c < p.norm_dim; c += kThreads) {
       float s = 0.f;
 #pragma unroll
       for (int k = 0; k < kWarps; ++k) s += red[k * p.norm_dim + c];
@@ -614,9 +700,14 @@ cudaError_t by_width(const NormRopeParams& p, Fn&& f) {
     const int v = p.n_freq ? p.n_freq / 8 : (g * np < nv / 2 ? g * np : nv / 2);
     return v <= g * np && nv - 2 * v <= g * nm;
   };
-#define DSA_TRY_SPLIT(G, NP, NM) \
-  if (fits(G, NP, NM))           \
-  return f(std::integral_constant<int, G>{}, std::integral_constant<int, NP>{}, std::integral_constant<int, NM>{})
+#define DSA_TRY_SPLIT(G, NP, NM)                                                                               \
+  if (fits(G, NP, NM)) {                                                                                       \
+    if (G <= 8 && Slots<G, NP, NM, (G <= 8)>::full(p))                                                         \
+      return f(std::integral_constant<int, G>{}, std::integral_constant<int, NP>{},                            \
+               std::integral_constant<int, NM>{}, std::integral_constant<bool, (G <= 8)>{});                   \
+    return f(std::integral_constant<int, G>{}, std::integral_constant<int, NP>{}, std::integral_constant<int, NM>{}, \
+             std::integral_constant<bool, false>{});                                                           \
+  }
   DSA_TRY_SPLIT(4, 1, 0);
   DSA_TRY_SPLIT(4, 1, 2);
   DSA_TRY_SPLIT(4, 1, 4);
@@ -627,26 +718,26 @@ cudaError_t by_width(const NormRopeParams& p, Fn&& f) {
   return cudaErrorInvalidValue;
 }
 
-// Steps and spans for blocks of `groups` rows a step; returns the grid.
+// Steps and spans for blocks of `groups` groups that hold `rows` rows a step; returns the grid.
 //   step: as many whole tokens as a block holds, but with few tokens only as many as spread
 //         them over the SMs; or part of a token's heads when a block holds less than one;
-//   span: steps whose angles together give every thread of the block one to fill in, as
-//         long as each block still gets four spans (their work then evens out), and at
-//         most 16 KB of angles.
-unsigned plan_walk(NormRopeParams& p, int groups, int sms, int blocks) {
+//   span: a block's even share of the tokens, or an even part of it when the angles of the
+//         share would take more than 16 KB.
+unsigned plan_walk(NormRopeParams& p, int groups, int rows, int sms, int blocks) {
   const long long n = p.n_tokens;
-  p.parts = (p.H + groups - 1) / groups;
+  p.parts = p.H <= rows ? 1 : (p.H + groups - 1) / groups;
   p.div_parts = fast_div((uint32_t)p.parts);
-  long long t = groups / p.H;
+  long long t = rows / p.H;
   const long long spread = (n + 2 * sms - 1) / (2 * sms);
   if (t > spread) t = spread;
   const long long table = p.n_freq ? 16384 / (8LL * p.n_freq) : t;
   if (t > table) t = table;
   p.tokens_per_step = t < 1 ? 1 : (int)t;
-  long long k = p.n_freq ? 256 / ((long long)p.tokens_per_step * p.n_freq) : 8;
-  const long long even = n / (4LL * blocks * p.tokens_per_step);
-  if (k > even) k = even;
-  p.span_tokens = p.tokens_per_step * (k < 1 ? 1 : (int)k);
+  const long long steps = (n + p.tokens_per_step - 1) / p.tokens_per_step, share = (steps + blocks - 1) / blocks;
+  long long most = p.n_freq ? 2048LL / ((long long)p.tokens_per_step * p.n_freq) : share;
+  if (most < 1) most = 1;
+  const long long rounds = (share + most - 1) / most, k = (steps + blocks * rounds - 1) / (blocks * rounds);
+  p.span_tokens = p.tokens_per_step * (int)k;
   p.n_spans = (int)((n + p.span_tokens - 1) / p.span_tokens);
   return (unsigned)(p.n_spans < blocks ? p.n_spans : blocks);
 }
@@ -655,20 +746,26 @@ unsigned plan_walk(NormRopeParams& p, int groups, int sms, int blocks) {
 
 cudaError_t launch_norm_rope(NormRopeParams p, int sms, cudaStream_t stream) {
   if (!p.n_freq) p.rot_start = 0;
-  return by_width(p, [&](auto g, auto np, auto nm) {
+  return by_width(p, [&](auto g, auto np, auto nm, auto full) {
     constexpr int G = decltype(g)::value, NP = decltype(np)::value, NM = decltype(nm)::value;
+    constexpr bool FULL = decltype(full)::value;
     const bool layer = p.norm == DSA_NORM_LAYER;
     const size_t params = (size_t)p.norm_dim * (p.b ? 2 : 1);
-    if (p.codes && p.H > kMaxThreads / G)
+    constexpr int kGroups = kThreads / G;
+    if (!p.codes) {
+      const unsigned grid = plan_walk(p, kGroups, kGroups, sms, sms * resident(2 * NP + NM, layer));
+      const size_t smem = ((size_t)p.span_tokens * p.n_freq * 4 + params) * sizeof(float);
+      return launch_pdl(layer ? norm_rope_kernel<G, NP, NM, FULL, true> : norm_rope_kernel<G, NP, NM, FULL, false>, dim3(grid),
+                        dim3(kThreads), smem, stream, p);
+    }
+    constexpr int R = 1;
+    if (p.H > R * kGroups)
       return launch_pdl(layer ? norm_rope_wide_kernel<G, NP, NM, true> : norm_rope_wide_kernel<G, NP, NM, false>,
-                        dim3(p.n_tokens), dim3(kMaxThreads), (2 * p.n_freq + params) * sizeof(float), stream, p);
-    // Twice the threads where that lets a block hold all heads of a token (e4m3).
-    const int threads = p.codes && p.H > 256 / G ? kMaxThreads : 256;
-    const unsigned grid = plan_walk(p, threads / G, sms, sms * (threads == 256 ? kBlocksPerSm : kBlocksPerSm / 2));
+                        dim3(p.n_tokens), dim3(kThreads), (2 * p.n_freq + params) * sizeof(float), stream, p);
+    const unsigned grid = plan_walk(p, kGroups, R * kGroups, sms, sms * 4);
     const size_t smem = ((size_t)p.span_tokens * p.n_freq * 4 + params + 3 * p.tokens_per_step) * sizeof(float);
-    auto kern = p.codes ? (layer ? norm_rope_kernel<G, NP, NM, true, true> : norm_rope_kernel<G, NP, NM, true, false>)
-                        : (layer ? norm_rope_kernel<G, NP, NM, false, true> : norm_rope_kernel<G, NP, NM, false, false>);
-    return launch_pdl(kern, dim3(grid), dim3(threads), smem, stream, p);
+    return launch_pdl(layer ? norm_rope_e4m3_kernel<G, NP, NM, FULL, R, true> : norm_rope_e4m3_kernel<G, NP, NM, FULL, R, false>,
+                      dim3(grid), dim3(kThreads), smem, stream, p);
   });
 }
 
@@ -677,15 +774,16 @@ int norm_rope_bwd_blocks(int sms) { return sms * kNormRopeBwdBlocksPerSm; }
 cudaError_t launch_norm_rope_bwd(NormRopeParams p, int sms, cudaStream_t stream) {
   if (!p.n_freq) p.rot_start = 0;
   int grid = 0;
-  const cudaError_t e = by_width(p, [&](auto g, auto np, auto nm) {
+  const cudaError_t e = by_width(p, [&](auto g, auto np, auto nm, auto full) {
     constexpr int G = decltype(g)::value, NP = decltype(np)::value, NM = decltype(nm)::value;
-    grid = (int)plan_walk(p, kBwdThreads / G, sms, norm_rope_bwd_blocks(sms));
+    constexpr bool FULL = decltype(full)::value;
+    grid = (int)plan_walk(p, kThreads / G, kThreads / G, sms, norm_rope_bwd_blocks(sms));
     size_t smem = ((size_t)p.span_tokens * p.n_freq * 4 + p.norm_dim * (p.b ? 2 : 1)) * sizeof(float);
-    const size_t red = (size_t)(kBwdThreads / 32) * p.norm_dim * sizeof(float);
+    const size_t red = (size_t)(kThreads / 32) * p.norm_dim * sizeof(float);
     if (red > smem) smem = red;
-    return launch_pdl(p.norm == DSA_NORM_LAYER ? norm_rope_bwd_kernel<G, NP, NM, true>
-                                               : norm_rope_bwd_kernel<G, NP, NM, false>,
-                      dim3(grid), dim3(kBwdThreads), smem, stream, p);
+    return launch_pdl(p.norm == DSA_NORM_LAYER ? norm_rope_bwd_kernel<G, NP, NM, FULL, true>
+                                               : norm_rope_bwd_kernel<G, NP, NM, FULL, false>,
+                      dim3(grid), dim3(kThreads), smem, stream, p);
   });
   if (e != cudaSuccess || p.norm == DSA_NORM_NONE) return e;
   return launch_pdl(norm_rope_sum_kernel, dim3((p.norm_dim + 31) / 32, p.b ? 2 : 1), dim3(256), 0, stream, p, grid);
