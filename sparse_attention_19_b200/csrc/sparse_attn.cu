@@ -77,15 +77,15 @@ enum AttnMode {
 // one warp per slot issues fast enough; that leaves room for a fourth value stage
 // (it also needs no staged index lists) and for 128 registers in every thread.
 //
-// kPacked: every key (value) loader warp converts its 8 rows of every chunk, so all of
-// them pass every slot.
+// kPacked: 16 loader warps convert; they read the index lists themselves (two warps only
+// stage the validity words), and the room of the staged lists goes to two key slots.
 //
 // Register split: a CTA of 768 threads launches with 80 registers per thread (6 warps
 // per SM sub-partition); the softmax warpgroup then takes 120 and the other
 // warpgroups (MMA issuers, loaders) keep 72.
 template <int MODE>
 struct Cfg {
-  static constexpr int kKStages = 6;                   // K-chunk ring depth (8 KB stages)
+  static constexpr int kKStages = MODE == kPacked ? 8 : 6;   // K-chunk ring depth (8 KB stages)
   static constexpr int kVStages = MODE == kWindow ? 4 : 3;   // V ring depth (64 keys x this CTA's value planes)
   static constexpr int kKTeamWarps = MODE == kWindow ? 1 : 3;
   static constexpr int kKTeamSlots = MODE == kWindow ? 1 : 2;
@@ -96,11 +96,14 @@ struct Cfg {
   static constexpr int kVWarps = MODE == kPacked ? 8 : kVStages * kVWarpsPerSlot;
   static constexpr int kThreads = 32 * (kVWarp0 + kVWarps);   // 768 (kWindow: 512)
   static constexpr int kStageWarps = MODE == kPacked ? 2 : kVWarps;   // warps that stage the indices
-  static constexpr int kFillers = MODE == kPacked ? 2 * kKWarps : 1;  // arrivals that fill a ring slot
+  // Arrivals that fill a key slot and a value slot (kPacked: 8 warps, or a team of 4 twice, and a
+  // team, of both CTAs).
+  static constexpr int kKFillers = MODE == kPacked ? 16 : 1, kVFillers = MODE == kPacked ? 8 : 1;
+  static constexpr int kIdxReaders = MODE == kPacked ? 0 : kKWarps + kVWarps;   // loader warps that read staged indices
   static constexpr bool kSplitRegs = kThreads > 512;
 };
-static_assert(Cfg<kPacked>::kKWarps == 8 && Cfg<kPacked>::kVWarps == 8, "8 warps x 8 rows convert 64 keys");
-constexpr int kMaxKStages = 6, kMaxVStages = 4;
+static_assert(Cfg<kPacked>::kKWarps == 8 && Cfg<kPacked>::kVWarps == 8, "two teams of four warps each");
+constexpr int kMaxKStages = 8, kMaxVStages = 4;
 constexpr int kStageBatch = 8;       // index words in flight per warp while staging
 constexpr uint32_t kRegsLaunch = 80;
 constexpr uint32_t kRegsSoftmax = 120;
@@ -241,185 +244,197 @@ __device__ __forceinline__ uint4 unpack_codes(uint32_t w, __nv_bfloat162 s, __nv
   return make_uint4(r[0], r[1], r[2], r[3]);
 }
 
-// 16 columns (two words) of row `r8` of an 8-row swizzle atom, from 16-byte column 2 * part.
-__device__ __forceinline__ void store_codes(uint8_t* atom, int r8, int part, uint32_t w0, uint32_t w1,
+// 16 columns (two words) to the 16-byte columns at lo and hi of a swizzled row.
+__device__ __forceinline__ void store_codes(uint8_t* row, uint32_t lo, uint32_t hi, uint32_t w0, uint32_t w1,
                                             uint32_t scale_bits) {
   const uint32_t dup = scale_bits | (scale_bits << 16);
   const __nv_bfloat162 s = *reinterpret_cast<const __nv_bfloat162*>(&dup);
   const __nv_bfloat162 off = __hmul2(s, __floats2bfloat162_rn(-24.f, -24.f));
-  uint8_t* row = atom + r8 * 128;
-  *reinterpret_cast<uint4*>(row + (((2 * part) ^ r8) * 16)) = unpack_codes(w0, s, off);
-  *reinterpret_cast<uint4*>(row + (((2 * part + 1) ^ r8) * 16)) = unpack_codes(w1, s, off);
+  *reinterpret_cast<uint4*>(row + lo) = unpack_codes(w0, s, off);
+  *reinterpret_cast<uint4*>(row + hi) = unpack_codes(w1, s, off);
 }
 
-// kPacked loaders walk the tiles of all their units one after the other; the loads of a
-// tile are issued while the tile before it is converted, across unit boundaries too.
+// kPacked loaders.  Teams of four warps own alternate jobs: a job is 64 rows x 128 columns of
+// 4-bit codes (two key chunks, or one value stage), 16 rows to a warp, four lanes to a row, 16
+// columns of both chunks to a lane and row.  The registers that held a job's codes are
+// loaded again for the next tile as soon as it is converted, so a tile of loads is in
+// flight across units too.
 struct TileCursor {
   Unit U;
   int u, j;               // unit (>= n_units: past the end) and tile
-  uint32_t ucount;        // units entered so far
+  __device__ __forceinline__ void start(const AttnParams& p, int cluster_id, int n_clusters) {
+    u = next_unit<kPacked>(p, cluster_id, n_clusters, U);
+    j = U.j0;
+  }
+  __device__ __forceinline__ void next(const AttnParams& p, int n_clusters) {
+    if (u >= p.n_units || ++j < U.j1) return;
+    u = next_unit<kPacked>(p, u + n_clusters, n_clusters, U);
+    j = U.j0;
+  }
+  // Cache row of slot x of the tile, -1 for a masked one.
+  __device__ __forceinline__ int row(const AttnParams& p, int x) const {
+    if (u >= p.n_units) return -1;
+    x += j * kTileKeys;
+    if (x >= p.k) return -1;
+    const int s = p.dense ? (x <= U.t ? x : -1) : __ldg(p.indices + (size_t)U.row * p.k + x);
+    return s >= 0 && s < p.Lk ? U.b * p.Lk + s : -1;
+  }
 };
 
-// Cache rows of this lane's slots in the cursor's tile: slot `x0` (and x0 + 64 when TWO),
-// -1 for a masked one.  Waits for the unit's staged indices on entering it and releases
-// them with its last tile.
-template <bool TWO>
-__device__ __forceinline__ bool cursor_rows(AttnBarriers& S, const int32_t* idx_sm, const TileCursor& c, int x0,
-                                            int& r0, int& r1, volatile uint32_t* abort_flag) {
-  const uint32_t ib = (c.ucount - 1) & 1u, uph = ((c.ucount - 1) >> 1) & 1u;
-  if (c.j == c.U.j0 && !mbar_wait_warp(&S.idx_full[ib], uph, abort_flag)) return false;
-  const int32_t* idx = idx_sm + ib * kMaxIdx + (c.j - c.U.j0) * kTileKeys + x0;
-  r0 = idx[0];
-  if (TWO) r1 = idx[kHalfKeys];
-  if (c.j == c.U.j1 - 1) {
-    __syncwarp();
-    if (lane_id() == 0) mbar_arrive(&S.idx_empty[ib]);
-  }
-  return true;
-}
-
-__device__ __forceinline__ void cursor_next(const AttnParams& p, TileCursor& c, int n_clusters) {
-  if (++c.j < c.U.j1) return;
-  c.u = next_unit<kPacked>(p, c.u + n_clusters, n_clusters, c.U);
-  c.j = c.U.j0;
-  ++c.ucount;
-}
-
-// Key loaders of kPacked: warp `pw` converts rows 8 pw .. 8 pw + 7 of this CTA's 64 keys,
-// four lanes to a row, 16 columns of every 64-column chunk to a lane.
+// Key loaders.  Per tile, team t does chunk pairs t and t + 2, and each of the eight warps 8
+// rows of the bf16 tail chunk.  Masked slots load some row: their logits are replaced.
 template <int NC, int DV>
-__device__ __forceinline__ void packed_keys(const AttnParams& p, AttnBarriers& S, uint8_t* k_sm,
-                                            const int32_t* idx_sm, int pw, uint32_t rank, int cluster_id,
-                                            int n_clusters, volatile uint32_t* abort_flag) {
+__device__ __forceinline__ void packed_keys(const AttnParams& p, AttnBarriers& S, uint8_t* k_sm, int pw,
+                                            uint32_t rank, int cluster_id, int n_clusters,
+                                            volatile uint32_t* abort_flag) {
   constexpr int kKStages = Cfg<kPacked>::kKStages;
-  constexpr int kLat = DV / 64;                        // chunks of 4-bit columns; then one bf16 tail chunk
+  constexpr int kLat = DV / 64, kQ = kLat / 2;         // chunks of 4-bit columns, in pairs; then one bf16 tail chunk
   static_assert(NC == kLat + 1, "one tail chunk");
-  const int lane = (int)lane_id(), r8 = lane / 4, part = lane % 4;
+  constexpr int kPairs = (kQ + 1) / 2;                 // of a team
+  const int lane = (int)lane_id(), r8 = lane / 4, part = lane % 4, team = pw / 4, w4 = pw % 4;
+  const int x0 = (int)rank * kHalfKeys + w4 * 16 + r8;
   TileCursor c;
-  c.u = next_unit<kPacked>(p, cluster_id, n_clusters, c.U);
+  c.start(p, cluster_id, n_clusters);
   if (c.u >= p.n_units) return;
-  c.j = c.U.j0;
-  c.ucount = 1;
-  const int x0 = (int)rank * kHalfKeys + pw * 8 + r8;
-  int row, unused;
-  if (!cursor_rows<false>(S, idx_sm, c, x0, row, unused, abort_flag)) return;
-  uint32_t code[kLat * 2], sc[kLat / 2];
-  uint4 tail[2];
-  // A masked row gets scale 0 and an all-zero tail: keys of zeros, no load.
-  auto load_code = [&](int q, int r) {                 // 16 bytes: chunks 2q, 2q + 1
-    uint4 v = make_uint4(0, 0, 0, 0);
-    if (r >= 0) v = __ldg(reinterpret_cast<const uint4*>(p.codes + (size_t)r * (DV / 2) + part * (DV / 8)) + q);
-    code[4 * q] = v.x; code[4 * q + 1] = v.y; code[4 * q + 2] = v.z; code[4 * q + 3] = v.w;
-  };
-  auto load_rest = [&](int r) {
-    const uint8_t* ss = reinterpret_cast<const uint8_t*>(p.scales) + (size_t)max(r, 0) * (DV / 16) + (part / 2) * (DV / 32);
-    if constexpr (kLat == 8) {
-      uint4 v = make_uint4(0, 0, 0, 0);
-      if (r >= 0) v = __ldg(reinterpret_cast<const uint4*>(ss));
-      sc[0] = v.x; sc[1] = v.y; sc[2] = v.z; sc[3] = v.w;
-    } else {
-      sc[0] = r >= 0 ? __ldg(reinterpret_cast<const uint32_t*>(ss)) : 0u;
-    }
-    const uint4* ts = reinterpret_cast<const uint4*>(p.tail + (size_t)max(r, 0) * 64) + part * 2;
-    tail[0] = tail[1] = make_uint4(0, 0, 0, 0);
-    if (r >= 0) { tail[0] = __ldg(ts); tail[1] = __ldg(ts + 1); }
-  };
+  uint4 code[kPairs][2], tail[2];
+  uint32_t sc[kPairs][2];
+  auto load_pair = [&](int i, int r0, int r1) {
+    const int q = 2 * i + team;
+    if (q >= kQ) return;
 #pragma unroll
-  for (int q = 0; q < kLat / 2; ++q) load_code(q, row);
-  load_rest(row);
-  uint32_t kc = 0;
-  while (c.u < p.n_units) {
-    cursor_next(p, c, n_clusters);
-    int next = -1;
+    for (int g = 0; g < 2; ++g) {
+      const size_t r = (size_t)max(g ? r1 : r0, 0);
+      code[i][g] = __ldg(reinterpret_cast<const uint4*>(p.codes + r * (DV / 2) + part * (DV / 8)) + q);
+      sc[i][g] = __ldg(reinterpret_cast<const uint32_t*>(p.scales + r * (DV / 32) + (part / 2) * (DV / 64)) + q);
+    }
+  };
+  auto load_tail = [&](int r0, int r1) {
+    const uint4* ts = reinterpret_cast<const uint4*>(p.tail + (size_t)max(team ? r1 : r0, 0) * 64) + part * 2;
+    tail[0] = __ldg(ts);
+    tail[1] = __ldg(ts + 1);
+  };
+  int r0 = c.row(p, x0), r1 = c.row(p, x0 + 8);
+#pragma unroll
+  for (int i = 0; i < kPairs; ++i) load_pair(i, r0, r1);
+  load_tail(r0, r1);
+  c.next(p, n_clusters);
+  r0 = c.row(p, x0);                                   // the next tile's rows
+  r1 = c.row(p, x0 + 8);
+  const uint32_t lo = ((2 * part) ^ r8) * 16, hi = ((2 * part + 1) ^ r8) * 16;
+  uint8_t* const out = k_sm + w4 * 2048 + r8 * 128;    // row group g: + 1024 g
+  const uint32_t full0 = mapa_shared(smem_u32(&S.k_full[0]), 0);
+  uint32_t tile_kc = 0;
+  for (;;) {
     const bool more = c.u < p.n_units;
-    if (more && !cursor_rows<false>(S, idx_sm, c, x0, next, unused, abort_flag)) return;
+    const int n0 = r0, n1 = r1;
+    c.next(p, n_clusters);
+    r0 = c.row(p, x0);                                 // two tiles ahead
+    r1 = c.row(p, x0 + 8);
 #pragma unroll
-    for (int ch = 0; ch < NC; ++ch, ++kc) {
-      const uint32_t st = kc % kKStages;
-      if (!mbar_wait_warp(&S.k_empty[st], ((kc / kKStages) & 1u) ^ 1u, abort_flag)) return;
-      uint8_t* atom = k_sm + st * kPlane64 + pw * 1024;
-      if (ch < kLat) {
-        const uint32_t sw = sc[ch / 2];
-        store_codes(atom, r8, part, code[2 * ch], code[2 * ch + 1], ch % 2 ? sw >> 16 : sw & 0xffffu);
-        if (ch % 2 == 1) load_code(ch / 2, next);
-      } else {
-        *reinterpret_cast<uint4*>(atom + r8 * 128 + (((2 * part) ^ r8) * 16)) = tail[0];
-        *reinterpret_cast<uint4*>(atom + r8 * 128 + (((2 * part + 1) ^ r8) * 16)) = tail[1];
-        load_rest(next);
+    for (int i = 0; i < kPairs; ++i) {
+      const int q = 2 * i + team;
+      if (q >= kQ) continue;
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const uint32_t kc = tile_kc + 2 * q + e, st = kc % kKStages;
+        if (!mbar_wait_warp(&S.k_empty[st], ((kc / kKStages) & 1u) ^ 1u, abort_flag)) return;
+#pragma unroll
+        for (int g = 0; g < 2; ++g)
+          store_codes(out + st * kPlane64 + g * 1024, lo, hi, e ? code[i][g].z : code[i][g].x,
+                      e ? code[i][g].w : code[i][g].y, e ? sc[i][g] >> 16 : sc[i][g] & 0xffffu);
+        if (e == 1 && more) load_pair(i, n0, n1);
+        fence_proxy_async_smem();
+        __syncwarp();
+        // a team fills the slot that all eight warps fill for the tail: two arrivals each
+        if (lane == 0) mbar_arrive_remote_n(full0 + st * 8, 2);
       }
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive_remote(mapa_shared(smem_u32(&S.k_full[st]), 0));
     }
+    const uint32_t kc = tile_kc + kLat, st = kc % kKStages;
+    if (!mbar_wait_warp(&S.k_empty[st], ((kc / kKStages) & 1u) ^ 1u, abort_flag)) return;
+    *reinterpret_cast<uint4*>(out + st * kPlane64 + team * 1024 + lo) = tail[0];
+    *reinterpret_cast<uint4*>(out + st * kPlane64 + team * 1024 + hi) = tail[1];
+    if (more) load_tail(n0, n1);
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) mbar_arrive_remote(full0 + st * 8);
     if (!more) break;
+    tile_kc += NC;
   }
 }
 
-// Value loaders of kPacked: warp `pw` converts rows 8 pw .. of both 64-key halves of the
-// tile, this CTA's value columns.
+// Value loaders.  Team t does the tile's stages t, t + 2: this CTA's half of the columns of a
+// value block, 64 rows.  A masked slot's row gets scale 0: zeros, whatever it holds.
 template <int DV>
-__device__ __forceinline__ void packed_values(const AttnParams& p, AttnBarriers& S, uint8_t* v_sm,
-                                              const int32_t* idx_sm, int pw, uint32_t rank, int cluster_id,
-                                              int n_clusters, volatile uint32_t* abort_flag) {
+__device__ __forceinline__ void packed_values(const AttnParams& p, AttnBarriers& S, uint8_t* v_sm, int pw,
+                                              uint32_t rank, int cluster_id, int n_clusters,
+                                              volatile uint32_t* abort_flag) {
   using VS = VShape<DV>;
   constexpr int kVStages = Cfg<kPacked>::kVStages;
   constexpr int kPl = VS::kPlanes;                     // 64-column planes of a stage
-  constexpr int kSt = 2 * VS::kNpv;                    // stages per tile: key half, value block
-  const int lane = (int)lane_id(), r8 = lane / 4, part = lane % 4;
+  constexpr int kJobs = VS::kNpv;                      // per tile and team (two key halves x kNpv blocks, two teams)
+  const int lane = (int)lane_id(), r8 = lane / 4, part = lane % 4, team = pw / 4, w4 = pw % 4;
+  // Stage s is key half s / kNpv, block s % kNpv; team t's job i is stage 2 i + t.
+  const int block = kJobs == 2 ? team : 0;
+  const int x0 = (kJobs == 2 ? 0 : team * kHalfKeys) + w4 * 16 + r8;   // job i: + 64 i
+  const int chunk = block * (VS::kN / 64) + (int)rank * kPl;           // of the stage's first plane
   TileCursor c;
-  c.u = next_unit<kPacked>(p, cluster_id, n_clusters, c.U);
+  c.start(p, cluster_id, n_clusters);
   if (c.u >= p.n_units) return;
-  c.j = c.U.j0;
-  c.ucount = 1;
-  const int x0 = pw * 8 + r8;
-  int row[2];
-  if (!cursor_rows<true>(S, idx_sm, c, x0, row[0], row[1], abort_flag)) return;
-  uint32_t code[kSt][2 * kPl], sc[kSt];
-  auto load = [&](int s, int r) {
-    // chunk of the stage's first plane: value block s % kNpv, this CTA's half of it
-    const int ch = (s % VS::kNpv) * (VS::kN / 64) + (int)rank * kPl;
-    const uint8_t* cs = p.codes + (size_t)max(r, 0) * (DV / 2) + part * (DV / 8) + ch * 8;
-    const __nv_bfloat16* ss = p.scales + (size_t)max(r, 0) * (DV / 32) + (part / 2) * (DV / 64) + ch;
-    if constexpr (kPl == 2) {
-      uint4 v = make_uint4(0, 0, 0, 0);
-      sc[s] = 0;
-      if (r >= 0) {
-        v = __ldg(reinterpret_cast<const uint4*>(cs));
-        sc[s] = __ldg(reinterpret_cast<const uint32_t*>(ss));
+  uint4 code[kJobs][2];
+  uint32_t sc[kJobs][2];
+  int row[kJobs][2];
+  auto rows = [&]() {
+#pragma unroll
+    for (int i = 0; i < kJobs; ++i)
+#pragma unroll
+      for (int g = 0; g < 2; ++g) row[i][g] = c.row(p, x0 + i * kHalfKeys + g * 8);
+  };
+  auto load = [&](int i, const int (&r)[2]) {
+#pragma unroll
+    for (int g = 0; g < 2; ++g) {
+      const size_t at = (size_t)max(r[g], 0);
+      const uint8_t* cs = p.codes + at * (DV / 2) + part * (DV / 8) + chunk * 8;
+      const __nv_bfloat16* ss = p.scales + at * (DV / 32) + (part / 2) * (DV / 64) + chunk;
+      if constexpr (kPl == 2) {
+        code[i][g] = __ldg(reinterpret_cast<const uint4*>(cs));
+        sc[i][g] = r[g] >= 0 ? __ldg(reinterpret_cast<const uint32_t*>(ss)) : 0u;
+      } else {
+        const uint2 v = __ldg(reinterpret_cast<const uint2*>(cs));
+        code[i][g] = make_uint4(v.x, v.y, 0u, 0u);
+        sc[i][g] = r[g] >= 0 ? __ldg(reinterpret_cast<const unsigned short*>(ss)) : 0u;
       }
-      code[s][0] = v.x; code[s][1] = v.y; code[s][2] = v.z; code[s][3] = v.w;
-    } else {
-      uint2 v = make_uint2(0, 0);
-      sc[s] = 0;
-      if (r >= 0) {
-        v = __ldg(reinterpret_cast<const uint2*>(cs));
-        sc[s] = __ldg(reinterpret_cast<const unsigned short*>(ss));
-      }
-      code[s][0] = v.x; code[s][1] = v.y;
     }
   };
+  rows();
 #pragma unroll
-  for (int s = 0; s < kSt; ++s) load(s, row[s / VS::kNpv]);
-  uint32_t vc = 0;
-  while (c.u < p.n_units) {
-    cursor_next(p, c, n_clusters);
-    int next[2] = {-1, -1};
+  for (int i = 0; i < kJobs; ++i) load(i, row[i]);
+  c.next(p, n_clusters);
+  rows();                                              // the next tile's
+  const uint32_t lo = ((2 * part) ^ r8) * 16, hi = ((2 * part + 1) ^ r8) * 16;
+  uint8_t* const out = v_sm + w4 * 2048 + r8 * 128;
+  const uint32_t full0 = mapa_shared(smem_u32(&S.v_full[0]), 0);
+  uint32_t st = (uint32_t)team, ph = 1;
+  for (;;) {
     const bool more = c.u < p.n_units;
-    if (more && !cursor_rows<true>(S, idx_sm, c, x0, next[0], next[1], abort_flag)) return;
 #pragma unroll
-    for (int s = 0; s < kSt; ++s, ++vc) {
-      const uint32_t st = vc % kVStages;
-      if (!mbar_wait_warp(&S.v_empty[st], ((vc / kVStages) & 1u) ^ 1u, abort_flag)) return;
+    for (int i = 0; i < kJobs; ++i) {
+      if (!mbar_wait_warp(&S.v_empty[st], ph, abort_flag)) return;
 #pragma unroll
       for (int pl = 0; pl < kPl; ++pl)
-        store_codes(v_sm + st * VS::kStageBytes + pl * kPlane64 + pw * 1024, r8, part, code[s][2 * pl],
-                    code[s][2 * pl + 1], pl ? sc[s] >> 16 : sc[s] & 0xffffu);
-      load(s, next[s / VS::kNpv]);
+#pragma unroll
+        for (int g = 0; g < 2; ++g)
+          store_codes(out + st * VS::kStageBytes + pl * kPlane64 + g * 1024, lo, hi, pl ? code[i][g].z : code[i][g].x,
+                      pl ? code[i][g].w : code[i][g].y, pl ? sc[i][g] >> 16 : sc[i][g] & 0xffffu);
+      if (more) load(i, row[i]);
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive_remote(mapa_shared(smem_u32(&S.v_full[st]), 0));
+      if (lane == 0) mbar_arrive_remote(full0 + st * 8);
+      st += 2;
+      if (st >= kVStages) { st -= kVStages; ph ^= 1u; }
     }
     if (!more) break;
+    c.next(p, n_clusters);
+    rows();
   }
 }
 
@@ -431,7 +446,7 @@ sparse_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
   using C = Cfg<MODE>;
   static_assert(NC <= kMaxChunks, "d_qk");
   constexpr int kKStages = C::kKStages, kVStages = C::kVStages, kKWarp0 = C::kKWarp0, kKWarps = C::kKWarps;
-  constexpr int kVWarp0 = C::kVWarp0, kVWarps = C::kVWarps, kKTeamWarps = C::kKTeamWarps;
+  [[maybe_unused]] constexpr int kVWarp0 = C::kVWarp0, kVWarps = C::kVWarps, kKTeamWarps = C::kKTeamWarps;
   constexpr int kKTeamSlots = C::kKTeamSlots, kVWarpsPerSlot = C::kVWarpsPerSlot, kStageWarps = C::kStageWarps;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   AttnBarriers& S = *reinterpret_cast<AttnBarriers*>(smem_raw);
@@ -455,8 +470,8 @@ sparse_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < kMaxChunks; ++i) { mbar_init(&S.q_full[i], 1); mbar_init(&S.q_empty[i], 1); }
-    for (int i = 0; i < kKStages; ++i) { mbar_init(&S.k_full[i], C::kFillers); mbar_init(&S.k_empty[i], 1); }
-    for (int i = 0; i < kVStages; ++i) { mbar_init(&S.v_full[i], C::kFillers); mbar_init(&S.v_empty[i], 1); }
+    for (int i = 0; i < kKStages; ++i) { mbar_init(&S.k_full[i], C::kKFillers); mbar_init(&S.k_empty[i], 1); }
+    for (int i = 0; i < kVStages; ++i) { mbar_init(&S.v_full[i], C::kVFillers); mbar_init(&S.v_empty[i], 1); }
     for (int i = 0; i < kPBufs; ++i) {
       mbar_init(&S.p_full[i], 8);      // 4 softmax warps x 2 CTAs
       mbar_init(&S.p_empty[i], 1);
@@ -465,7 +480,7 @@ sparse_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
       mbar_init(&S.s_full[i], 1);
       mbar_init(&S.s_empty[i], 8);     // 4 softmax warps x 2 CTAs
       mbar_init(&S.idx_full[i], kStageWarps);
-      mbar_init(&S.idx_empty[i], 4 + kKWarps + kVWarps);   // softmax warps + loader warps
+      mbar_init(&S.idx_empty[i], 4 + C::kIdxReaders);   // softmax warps + loader warps
     }
     mbar_init(&S.o_full, 1);
     mbar_init(&S.o_empty, 8);
@@ -492,8 +507,8 @@ sparse_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
   // Index staging (one warp of kStageWarps, number pw): each unit's selected positions
   // [j0*128, j1*128) go into buffer (unit ordinal % 2), one unit ahead, as the kv row to
   // load -- batch offset applied; padding and out-of-range entries gather row b*Lk
-  // (kPacked: -1, nothing is loaded) and are masked -- plus one validity ballot per 32
-  // positions for the softmax.  Warp pw stages the 32-position words pw, pw + kStageWarps,
+  // and are masked -- plus one validity ballot per 32 positions for the softmax
+  // (kPacked: only the ballots).  Warp pw stages the 32-position words pw, pw + kStageWarps,
   // ...  A buffer is free again once the loaders and the softmax warps are done with
   // the unit two back.
   auto stage = [&](const Unit& V, uint32_t buf, int pw) {
@@ -510,7 +525,6 @@ sparse_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
         const bool valid = x <= V.t && x < p.k;
         const uint32_t bal = __ballot_sync(0xffffffffu, valid);
         if (lane == 0) vmask[w] = bal;
-        if (MODE == kPacked) dst[w * 32 + (int)lane] = valid ? V.b * p.Lk + x : -1;
         if (leader && x < p.k) io[x] = valid ? x : -1;
       }
       if (leader && V.split == 0) {
@@ -534,8 +548,7 @@ sparse_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
         const int w = w0 + e * kStageWarps;
         if (w >= nwords) break;                       // warp-uniform
         const bool valid = (sidx[e] >= 0) && (sidx[e] < p.Lk);
-        if (MODE == kPacked) dst[w * 32 + (int)lane] = valid ? V.b * p.Lk + sidx[e] : -1;
-        else dst[w * 32 + (int)lane] = V.b * p.Lk + (valid ? sidx[e] : 0);   // validity: the ballot below
+        if (MODE != kPacked) dst[w * 32 + (int)lane] = V.b * p.Lk + (valid ? sidx[e] : 0);   // validity: the ballot below
         const uint32_t bal = __ballot_sync(0xffffffffu, valid);
         if (lane == 0) vmask[w] = bal;
       }
@@ -550,9 +563,9 @@ sparse_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
       // ------------------------------------------------------------------ converting loaders
       if constexpr (MODE == kPacked) {
         if (warp < kVWarp0)
-          packed_keys<NC, DV>(p, S, k_sm, idx_sm, (int)warp - kKWarp0, rank, cluster_id, n_clusters, abort_flag);
+          packed_keys<NC, DV>(p, S, k_sm, (int)warp - kKWarp0, rank, cluster_id, n_clusters, abort_flag);
         else
-          packed_values<DV>(p, S, v_sm, idx_sm, (int)warp - kVWarp0, rank, cluster_id, n_clusters, abort_flag);
+          packed_values<DV>(p, S, v_sm, (int)warp - kVWarp0, rank, cluster_id, n_clusters, abort_flag);
       }
     } else if (MODE == kPacked && warp > kPvWarp) {
       // ------------------------------------------------------------------ Q planes and index staging
@@ -1090,7 +1103,7 @@ cudaError_t launch_t(const AttnParams& p, const CUtensorMap& tq, const CUtensorM
                           + (size_t)C::kKStages * kPlane64         // K ring
                           + (size_t)C::kVStages * VShape<DV>::kStageBytes   // V ring
                           + (size_t)kPBufs * 2 * kPlane64          // P buffers (keys 0-63, 64-127 each)
-                          + (MODE == kWindow ? 0 : 2 * (size_t)kMaxIdx * sizeof(int32_t));   // staged indices, two units
+                          + (MODE == kSelected ? 2 * (size_t)kMaxIdx * sizeof(int32_t) : 0);   // staged indices, two units
   static_assert(smem <= 232448, "shared memory of one CTA");
   auto kern = sparse_attn_kernel<NC, DV, MODE>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
