@@ -262,22 +262,39 @@ __device__ __forceinline__ void store_codes(uint8_t* row, uint32_t lo, uint32_t 
 struct TileCursor {
   Unit U;
   int u, j;               // unit (>= n_units: past the end) and tile
+  const int32_t* list;    // the tile's index entries
+  int left, base;         // entries of the list from there on; cache row of the sequence's row 0
+  __device__ __forceinline__ void enter(const AttnParams& p) {
+    j = U.j0;
+    list = p.indices + (size_t)U.row * p.k + j * kTileKeys;
+    left = u < p.n_units ? p.k - j * kTileKeys : 0;
+    base = U.b * p.Lk;
+  }
   __device__ __forceinline__ void start(const AttnParams& p, int cluster_id, int n_clusters) {
     u = next_unit<kPacked>(p, cluster_id, n_clusters, U);
-    j = U.j0;
+    enter(p);
   }
   __device__ __forceinline__ void next(const AttnParams& p, int n_clusters) {
-    if (u >= p.n_units || ++j < U.j1) return;
-    u = next_unit<kPacked>(p, u + n_clusters, n_clusters, U);
-    j = U.j0;
+    if (u >= p.n_units) return;
+    if (++j < U.j1) {
+      list += kTileKeys;
+      left -= kTileKeys;
+    } else {
+      u = next_unit<kPacked>(p, u + n_clusters, n_clusters, U);
+      enter(p);
+    }
   }
-  // Cache row of slot x of the tile, -1 for a masked one.
+  // Entry x of the tile, as the cache row; -1 for a masked one.
   __device__ __forceinline__ int row(const AttnParams& p, int x) const {
-    if (u >= p.n_units) return -1;
-    x += j * kTileKeys;
-    if (x >= p.k) return -1;
-    const int s = p.dense ? (x <= U.t ? x : -1) : __ldg(p.indices + (size_t)U.row * p.k + x);
-    return s >= 0 && s < p.Lk ? U.b * p.Lk + s : -1;
+    if (x >= left) return -1;
+    int s;
+    if (p.dense) {
+      s = j * kTileKeys + x;
+      if (s > U.t) return -1;
+    } else {
+      s = __ldg(list + x);
+    }
+    return (unsigned)s < (unsigned)p.Lk ? base + s : -1;
   }
 };
 
@@ -334,20 +351,20 @@ __device__ __forceinline__ void packed_keys(const AttnParams& p, AttnBarriers& S
     for (int i = 0; i < kPairs; ++i) {
       const int q = 2 * i + team;
       if (q >= kQ) continue;
+      // Slots are freed in order: when the pair's second is free, so is its first.
+      const uint32_t kc = tile_kc + 2 * q, s0 = kc % kKStages, s1 = (kc + 1) % kKStages;
+      if (!mbar_wait_warp(&S.k_empty[s1], (((kc + 1) / kKStages) & 1u) ^ 1u, abort_flag)) return;
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const uint32_t kc = tile_kc + 2 * q + e, st = kc % kKStages;
-        if (!mbar_wait_warp(&S.k_empty[st], ((kc / kKStages) & 1u) ^ 1u, abort_flag)) return;
+      for (int e = 0; e < 2; ++e)
 #pragma unroll
         for (int g = 0; g < 2; ++g)
-          store_codes(out + st * kPlane64 + g * 1024, lo, hi, e ? code[i][g].z : code[i][g].x,
+          store_codes(out + (e ? s1 : s0) * kPlane64 + g * 1024, lo, hi, e ? code[i][g].z : code[i][g].x,
                       e ? code[i][g].w : code[i][g].y, e ? sc[i][g] >> 16 : sc[i][g] & 0xffffu);
-        if (e == 1 && more) load_pair(i, n0, n1);
-        fence_proxy_async_smem();
-        __syncwarp();
-        // a team fills the slot that all eight warps fill for the tail: two arrivals each
-        if (lane == 0) mbar_arrive_remote_n(full0 + st * 8, 2);
-      }
+      if (more) load_pair(i, n0, n1);
+      fence_proxy_async_smem();
+      __syncwarp();
+      // a team fills the slots that all eight warps fill for the tail: two arrivals each
+      if (lane < 2) mbar_arrive_remote_n(full0 + (lane ? s1 : s0) * 8, 2);
     }
     const uint32_t kc = tile_kc + kLat, st = kc % kKStages;
     if (!mbar_wait_warp(&S.k_empty[st], ((kc / kKStages) & 1u) ^ 1u, abort_flag)) return;
