@@ -395,12 +395,20 @@ def _on(device, stream, call):
     the stream that it launches on (a workspace freed on return is then reused in that
     stream's order)."""
     if stream is None and device.index == torch.cuda.current_device():
-        return call(torch._C._cuda_getCurrentRawStream(device.index))
+        return call(torch._C._cuda_getCurrentRawStream(device.index))   # as an integer: a Stream object costs 3 us
     if stream is not None and stream.device != device:
         raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
     with torch.cuda.device(device):
         with torch.cuda.stream(stream if stream is not None else torch.cuda.current_stream(device)):
             return call(ctypes.c_void_p(torch.cuda.current_stream().cuda_stream))
+
+
+def _like(t, dtype, shape, device):
+    """torch.empty of this shape and type; from a contiguous tensor of the same shape where
+    there is one (half the host time)."""
+    if t is not None and t.shape == shape and t.is_contiguous():
+        return torch.empty_like(t, dtype=dtype)
+    return torch.empty(shape, dtype=dtype, device=device)
 
 
 _NORMS = {None: 0, "rms": 1, "layer": 2}
@@ -453,7 +461,7 @@ def norm_rope(x, inv_freq=None, *, weight=None, bias=None, norm=None, norm_dim=N
     scale [B, L]) that the indexer takes.  ``out`` must not overlap ``x``.
     """
     a = _norm_rope_args(x, inv_freq, weight, bias, norm, norm_dim, eps, rot_start, interleaved, positions, q_offset)
-    dev, shape = x.device, tuple(x.shape)
+    dev, shape = x.device, x.shape
     out_t = torch.float8_e4m3fn if e4m3 else torch.bfloat16
     if not e4m3 and scale is not None:
         raise ValueError("scale belongs to the e4m3 output")
@@ -461,14 +469,16 @@ def norm_rope(x, inv_freq=None, *, weight=None, bias=None, norm=None, norm_dim=N
     def call(st):
         o, sc = out, scale
         if o is None:
-            o = torch.empty(shape, dtype=out_t, device=dev)
+            o = _like(x, out_t, shape, dev)
         else:
             _need_at(o, torch.uint8 if e4m3 and o.dtype == torch.uint8 else out_t, shape, "out", dev)
         if e4m3:
             if sc is None:
-                sc = torch.empty(shape[:2], dtype=torch.float32, device=dev)
-            _need_at(sc, torch.float32, shape[:2], "scale", dev)
-        _check(lib().dsa_norm_rope(ctypes.byref(a), o.data_ptr(), _ptr(sc), st), "dsa_norm_rope")
+                sc = _like(positions, torch.float32, shape[:2], dev)
+            else:
+                _need_at(sc, torch.float32, shape[:2], "scale", dev)
+        _check(lib().dsa_norm_rope(ctypes.byref(a), o.data_ptr(), None if sc is None else sc.data_ptr(), st),
+               "dsa_norm_rope")
         return (o, sc) if e4m3 else o
 
     return _on(dev, stream, call)
@@ -480,28 +490,30 @@ def norm_rope_bwd(dy, x, inv_freq=None, *, weight=None, bias=None, norm=None, no
     """Gradient of norm_rope's bf16 output: (dx bf16 [B, L, H, D], dweight fp32 or None,
     dbias fp32 or None) for ``dy`` bf16 [B, L, H, D]; the other arguments as in the forward."""
     a = _norm_rope_args(x, inv_freq, weight, bias, norm, norm_dim, eps, rot_start, interleaved, positions, q_offset)
-    dev, shape = x.device, tuple(x.shape)
+    dev, shape = x.device, x.shape
     _need_at(dy, torch.bfloat16, shape, "dy", dev)
 
     def call(st):
         gx, gw, gb, ws = dx, dweight, dbias, workspace
         if gx is None:
-            gx = torch.empty(shape, dtype=torch.bfloat16, device=dev)
-        _need_at(gx, torch.bfloat16, shape, "dx", dev)
+            gx = torch.empty_like(dy)
+        else:
+            _need_at(gx, torch.bfloat16, shape, "dx", dev)
         if norm is not None:
+            of_w = (a.norm_dim,)
             if gw is None:
-                gw = torch.empty(a.norm_dim, dtype=torch.float32, device=dev)
-            _need_at(gw, torch.float32, (a.norm_dim,), "dweight", dev)
-            if gb is None and bias is not None:
-                gb = torch.empty(a.norm_dim, dtype=torch.float32, device=dev)
-            if gb is not None:
-                _need_at(gb, torch.float32, (a.norm_dim,), "dbias", dev)
+                gw = _like(weight, torch.float32, of_w, dev)
+            else:
+                _need_at(gw, torch.float32, of_w, "dweight", dev)
+            if gb is None:
+                gb = None if bias is None else _like(bias, torch.float32, of_w, dev)
+            else:
+                _need_at(gb, torch.float32, of_w, "dbias", dev)
             if ws is None:
-                ws = torch.empty(max(16, lib().dsa_norm_rope_bwd_workspace(ctypes.byref(a))), dtype=torch.uint8,
-                                 device=dev)
+                ws = torch.empty(lib().dsa_norm_rope_bwd_workspace(ctypes.byref(a)), dtype=torch.uint8, device=dev)
         nbytes = 0 if ws is None else ws.numel() * ws.element_size()
-        _check(lib().dsa_norm_rope_bwd(ctypes.byref(a), dy.data_ptr(), gx.data_ptr(), _ptr(gw), _ptr(gb), _ptr(ws),
-                                       nbytes, st), "dsa_norm_rope_bwd")
+        _check(lib().dsa_norm_rope_bwd(ctypes.byref(a), dy.data_ptr(), gx.data_ptr(), _ptr(gw), _ptr(gb),
+                                       None if ws is None else ws.data_ptr(), nbytes, st), "dsa_norm_rope_bwd")
         return gx, gw, gb
 
     return _on(dev, stream, call)
@@ -550,8 +562,11 @@ def kv4_read(codes, scales, tail, L, start=None, offset=0, kv=None, stream=None)
         _need_at(start, torch.int32, (c.B,), "start", dev)
 
     def call(st):
-        o = torch.empty(c.B, L, c.d_qk, dtype=torch.bfloat16, device=dev) if kv is None else kv
-        _need_at(o, torch.bfloat16, (c.B, L, c.d_qk), "kv", dev)
+        o = kv
+        if o is None:
+            o = torch.empty((c.B, L, c.d_qk), dtype=torch.bfloat16, device=dev)
+        else:
+            _need_at(o, torch.bfloat16, (c.B, L, c.d_qk), "kv", dev)
         _check(lib().dsa_kv4_read(ctypes.byref(c), o.data_ptr(), L, _ptr(start), int(offset), st), "dsa_kv4_read")
         return o
 
