@@ -260,6 +260,12 @@ __device__ __forceinline__ void store_codes(uint8_t* row, uint32_t lo, uint32_t 
 // columns of both chunks to a lane and row.  The registers that held a job's codes are
 // loaded again for the next tile as soon as it is converted, so a tile of loads is in
 // flight across units too.
+// What sets the pace is the converting warps' instruction stream: without the conversions'
+// arithmetic 861 -> 682 us (1024 rows x 2048 keys), without their loads 726, without their
+// stores no gain, without all three 420.  So: one wait and one fence per job, not per chunk (822),
+// the two chunks of a job in a rolled loop, since 24 warps in five roles also wait for
+// instructions (754 -> 734); all eight warps in every chunk (986), one more team of key
+// warps at 56 registers (923), or the tail chunk gathered by the staging warps (779) were slower.
 struct TileCursor {
   Unit U;
   int u, j;               // unit (>= n_units: past the end) and tile
@@ -355,12 +361,16 @@ __device__ __forceinline__ void packed_keys(const AttnParams& p, AttnBarriers& S
       // Slots are freed in order: when the pair's second is free, so is its first.
       const uint32_t kc = tile_kc + 2 * q, s0 = kc % kKStages, s1 = (kc + 1) % kKStages;
       if (!mbar_wait_warp(&S.k_empty[s1], (((kc + 1) / kKStages) & 1u) ^ 1u, abort_flag)) return;
+#pragma unroll 1
+      for (int e = 0; e < 2; ++e) {
 #pragma unroll
-      for (int e = 0; e < 2; ++e)
-#pragma unroll
-        for (int g = 0; g < 2; ++g)
-          store_codes(out + (e ? s1 : s0) * kPlane64 + g * 1024, lo, hi, e ? code[i][g].z : code[i][g].x,
-                      e ? code[i][g].w : code[i][g].y, e ? sc[i][g] >> 16 : sc[i][g] & 0xffffu);
+        for (int g = 0; g < 2; ++g) {
+          store_codes(out + (e ? s1 : s0) * kPlane64 + g * 1024, lo, hi, code[i][g].x, code[i][g].y, sc[i][g] & 0xffffu);
+          code[i][g].x = code[i][g].z;
+          code[i][g].y = code[i][g].w;
+          sc[i][g] >>= 16;
+        }
+      }
       if (more) load_pair(i, n0, n1);
       fence_proxy_async_smem();
       __syncwarp();
@@ -437,12 +447,17 @@ __device__ __forceinline__ void packed_values(const AttnParams& p, AttnBarriers&
 #pragma unroll
     for (int i = 0; i < kJobs; ++i) {
       if (!mbar_wait_warp(&S.v_empty[st], ph, abort_flag)) return;
+#pragma unroll 1
+      for (int pl = 0; pl < kPl; ++pl) {
 #pragma unroll
-      for (int pl = 0; pl < kPl; ++pl)
-#pragma unroll
-        for (int g = 0; g < 2; ++g)
-          store_codes(out + st * VS::kStageBytes + pl * kPlane64 + g * 1024, lo, hi, pl ? code[i][g].z : code[i][g].x,
-                      pl ? code[i][g].w : code[i][g].y, pl ? sc[i][g] >> 16 : sc[i][g] & 0xffffu);
+        for (int g = 0; g < 2; ++g) {
+          store_codes(out + st * VS::kStageBytes + pl * kPlane64 + g * 1024, lo, hi, code[i][g].x, code[i][g].y,
+                      sc[i][g] & 0xffffu);
+          code[i][g].x = code[i][g].z;
+          code[i][g].y = code[i][g].w;
+          sc[i][g] >>= 16;
+        }
+      }
       if (more) load(i, row[i]);
       fence_proxy_async_smem();
       __syncwarp();
