@@ -209,6 +209,13 @@ __device__ __forceinline__ int window_key(const Unit& U, int x) {
   return x < U.n_sinks ? x : U.lo + (x - U.n_sinks);
 }
 
+// kWindow: whether the unit's last tile has no valid slot in its second 64: then the values of
+// that half, which would be multiplied by zeros, are neither loaded nor multiplied.
+template <int MODE>
+__device__ __forceinline__ bool one_half(const Unit& U) {
+  return MODE == kWindow && U.n_valid - (U.j1 - 1) * kTileKeys <= kHalfKeys;
+}
+
 // kWindow: 64 rows (slots x0 ..) of 64 columns from column col into a plane, lanes 0-15,
 // four rows each: one box per 16 rows that are consecutive keys, else gathers of four.
 // Either way 8 KB complete on the barrier.
@@ -758,7 +765,7 @@ sparse_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
         // then value block h); stage x goes to slot x % kVStages, and this warp visits
         // only its own slot's stages.
         constexpr uint32_t kPerTile = 2u * VS::kNpv;
-        const uint32_t vc_u = vc, nv = (uint32_t)(U.j1 - U.j0) * kPerTile;
+        const uint32_t vc_u = vc, nv = (uint32_t)(U.j1 - U.j0) * kPerTile - (one_half<MODE>(U) ? VS::kNpv : 0);
         for (uint32_t x = vc_u + (my_slot + kVStages - vc_u % kVStages) % kVStages; x < vc_u + nv && ok;
              x += kVStages) {
           const uint32_t st = my_slot, ph = (x / kVStages) & 1u;
@@ -870,7 +877,8 @@ sparse_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
             if (ok && first) ok = mbar_wait(&S.o_empty, (oc & 1u) ^ 1u, abort_flag, true);
             if (!ok) break;
             tc_fence_after();
-            for (int kh = 0; kh < 2 && ok; ++kh) {
+            const int halves = j == U.j1 - 1 && one_half<MODE>(U) ? 1 : 2;
+            for (int kh = 0; kh < halves && ok; ++kh) {
               for (int h = 0; h < VS::kNpv; ++h) {
                 const uint32_t st = vc % kVStages, ph = (vc / kVStages) & 1u;
                 if (!mbar_wait(&S.v_full[st], ph, abort_flag, MODE == kPacked)) { ok = false; break; }
