@@ -25,6 +25,7 @@
 #include <cstdint>
 
 #include "dsa_internal.h"
+#include "kv4.cuh"
 #include "ptx.cuh"
 
 namespace dsa {
@@ -81,13 +82,20 @@ __global__ void __launch_bounds__(kThreads) kv4_write_kernel(const Kv4Params p) 
   if (bad) step = __uint_as_float(0x7fc00000u);
   uint32_t code[2] = {0x88888888u, 0x88888888u};
   if (!zero && !bad) {
+    // The quotient as one multiplication by the rounded reciprocal and Markstein's correction
+    // by the residual (exact in a fused multiply-add), which rounds it correctly: a value
+    // halfway between two codes stays there.  Adding 1.5 * 2^23 + 8 then rounds it to
+    // the nearest integer, ties to even, and leaves q + 8 in the sum's low bits.
+    const float inv = __frcp_rn(step);
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
       code[k] = 0;
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        const int q = __float2int_rn(__fdiv_rn(x[8 * k + e], step)) + 8;
-        code[k] |= (uint32_t)q << (4 * (e / 2 + 4 * (e % 2)));
+        const float v = x[8 * k + e], q0 = v * inv;
+        const float q = fmaf(fmaf(-q0, step, v), inv, q0);
+        const uint32_t n = __float_as_uint(q + 12582920.f) & 15u;
+        code[k] |= n << (4 * (e / 2 + 4 * (e % 2)));
       }
     }
   }
@@ -109,27 +117,18 @@ __global__ void __launch_bounds__(kThreads) kv4_read_kernel(const Kv4Params p) {
   if (row >= p.B * p.L) return;
   const long long at = cache_row(p, row / p.L, row % p.L);
   const int tail8 = (p.d_qk - DV) / 8, c = lane / 4, part = lane % 4;
-  uint32_t w[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-  uint4 t = make_uint4(0, 0, 0, 0);
+  uint4 v[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)}, t = v[0];
   if (at >= 0) {
     const uint2 code = __ldg(reinterpret_cast<const uint2*>(p.codes + (size_t)at * (DV / 2) + part * (DV / 8) + c * 8));
-    const float step = __bfloat162float(p.scales[(size_t)at * (DV / 32) + (part / 2) * (DV / 64) + c]);
+    const Kv4Step step = kv4_step(reinterpret_cast<const unsigned short*>(
+        p.scales)[(size_t)at * (DV / 32) + (part / 2) * (DV / 64) + c]);
     if (lane < tail8) t = __ldg(reinterpret_cast<const uint4*>(p.tail + (size_t)at * (p.d_qk - DV)) + lane);
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      const uint32_t cw = k ? code.y : code.x;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {                   // columns 2i and 2i + 1 sit 4 nibbles apart
-        const float lo = (float)((int)((cw >> (4 * i)) & 15u) - 8) * step;
-        const float hi = (float)((int)((cw >> (4 * i + 16)) & 15u) - 8) * step;
-        const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
-        w[4 * k + i] = *reinterpret_cast<const uint32_t*>(&b);
-      }
-    }
+    v[0] = unpack_codes(code.x, step);
+    v[1] = unpack_codes(code.y, step);
   }
   uint4* dst = reinterpret_cast<uint4*>(p.out + (size_t)row * p.d_qk);
-  dst[2 * lane] = make_uint4(w[0], w[1], w[2], w[3]);
-  dst[2 * lane + 1] = make_uint4(w[4], w[5], w[6], w[7]);
+  dst[2 * lane] = v[0];
+  dst[2 * lane + 1] = v[1];
   if (lane < tail8) dst[DV / 8 + lane] = t;
 }
 

@@ -49,6 +49,7 @@
 #include <cstdint>
 
 #include "dsa_internal.h"
+#include "kv4.cuh"
 #include "ptx.cuh"
 
 namespace dsa {
@@ -236,30 +237,12 @@ __device__ __forceinline__ void window_load(const AttnParams& p, const Unit& U, 
   }
 }
 
-// kPacked: 8 columns of the 4-bit cache as bf16.  Nibble n stands for n - 8: put at bits
-// 3-6 of bf16's 16.0 it makes 16 + n, and one fused multiply-add (16 + n) * s - 24 s gives
-// (n - 8) s exactly, since s has 5 significant bits and |n - 8| 3 (and 24 s is exact).
-__device__ __forceinline__ uint4 unpack_codes(uint32_t w, __nv_bfloat162 s, __nv_bfloat162 off) {
-  uint32_t r[4];
-#pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    const uint32_t sh = k == 0 ? w << 3 : w >> (4 * k - 3);
-    uint32_t b = (sh & 0x00780078u) | 0x41804180u;
-    __nv_bfloat162 v = *reinterpret_cast<__nv_bfloat162*>(&b);
-    v = __hfma2(v, s, off);
-    r[k] = *reinterpret_cast<uint32_t*>(&v);
-  }
-  return make_uint4(r[0], r[1], r[2], r[3]);
-}
-
 // 16 columns (two words) to the 16-byte columns at lo and hi of a swizzled row.
 __device__ __forceinline__ void store_codes(uint8_t* row, uint32_t lo, uint32_t hi, uint32_t w0, uint32_t w1,
                                             uint32_t scale_bits) {
-  const uint32_t dup = scale_bits | (scale_bits << 16);
-  const __nv_bfloat162 s = *reinterpret_cast<const __nv_bfloat162*>(&dup);
-  const __nv_bfloat162 off = __hmul2(s, __floats2bfloat162_rn(-24.f, -24.f));
-  *reinterpret_cast<uint4*>(row + lo) = unpack_codes(w0, s, off);
-  *reinterpret_cast<uint4*>(row + hi) = unpack_codes(w1, s, off);
+  const Kv4Step t = kv4_step(scale_bits);
+  *reinterpret_cast<uint4*>(row + lo) = unpack_codes(w0, t);
+  *reinterpret_cast<uint4*>(row + hi) = unpack_codes(w1, t);
 }
 
 // kPacked loaders.  Teams of four warps own alternate jobs: a job is 64 rows x 128 columns of
