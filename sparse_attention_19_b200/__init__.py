@@ -403,6 +403,11 @@ def _on(device, stream, call):
             return call(ctypes.c_void_p(torch.cuda.current_stream().cuda_stream))
 
 
+def _need_workspace(ws, device):
+    if ws is not None and (not isinstance(ws, torch.Tensor) or ws.device != device or not ws.is_contiguous()):
+        raise ValueError(f"workspace must be a contiguous tensor on {device}")
+
+
 def _like(t, dtype, shape, device):
     """torch.empty of this shape and type; from a contiguous tensor of the same shape where
     there is one (half the host time)."""
@@ -492,6 +497,7 @@ def norm_rope_bwd(dy, x, inv_freq=None, *, weight=None, bias=None, norm=None, no
     a = _norm_rope_args(x, inv_freq, weight, bias, norm, norm_dim, eps, rot_start, interleaved, positions, q_offset)
     dev, shape = x.device, x.shape
     _need_at(dy, torch.bfloat16, shape, "dy", dev)
+    _need_workspace(workspace, dev)
 
     def call(st):
         gx, gw, gb, ws = dx, dweight, dbias, workspace
@@ -599,6 +605,7 @@ def sparse_attn_kv4(q, codes, scales, tail, indices, scale, out=None, lse=None, 
     c, a = _kv4_attn_args(q, codes, scales, tail, scale)
     dev, Lq, k = q.device, q.shape[1], indices.shape[-1]
     _need_at(indices, torch.int32, (c.B, Lq, k), "indices", dev)
+    _need_workspace(workspace, dev)
 
     def call(st):
         o, l = _attn_outputs(c.B, Lq, a.H, c.d_v, out, lse, want_lse, dev)
@@ -616,9 +623,12 @@ def forward_kv4(q_I, q_scale, w, k_I, k_scale, q, codes, scales, tail, k, scale,
     c, a = _kv4_attn_args(q, codes, scales, tail, scale)
     dev = q.device
     ia = _indexer_args(q_I, q_scale, w, k_I, k_scale, q_offset)
-    if (ia.B, ia.Lq, ia.Lk) != (c.B, q.shape[1], c.Lk) or w.device != dev:
-        raise ValueError(f"the indexer's B, Lq, Lk {(ia.B, ia.Lq, ia.Lk)} on {w.device} differ from the attention's "
-                         f"{(c.B, q.shape[1], c.Lk)} on {dev}")
+    if (ia.B, ia.Lq, ia.Lk) != (c.B, q.shape[1], c.Lk):
+        raise ValueError(f"the indexer's B, Lq, Lk {(ia.B, ia.Lq, ia.Lk)} differ from the attention's "
+                         f"{(c.B, q.shape[1], c.Lk)}")
+    if any(t is not None and t.device != dev for t in (q_I, q_scale, w, k_I, k_scale)):
+        raise ValueError(f"the indexer's tensors must be on {dev}")
+    _need_workspace(workspace, dev)
     if sel_scores is not None:
         _need_at(sel_scores, torch.float32, (ia.B, ia.Lq, k), "sel_scores", dev)
 
@@ -649,6 +659,7 @@ def window_attn(q, kv, d_v, scale, window, sinks=0, q_offset=0, start=None, out=
         raise ValueError(f"kv is on {kv.device}, expected {dev}")
     if start is not None:
         _need_at(start, torch.int32, (B,), "start", dev)
+    _need_workspace(workspace, dev)
     window, sinks = min(int(window), 2 ** 31 - 1), min(int(sinks), 2 ** 31 - 1)
 
     def call(st):

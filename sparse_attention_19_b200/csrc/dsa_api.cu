@@ -1,7 +1,7 @@
 // dsa_api.cu -- the C ABI of libdsa.so (declared in include/dsa.h): argument
 // checks, TMA descriptor set-up, workspace layout and kernel dispatch for the
 // DeepSeek Sparse Attention forward pass.  Every step of the computation runs in
-// the kernels of indexer.cu, topk.cu, sparse_attn.cu and indexer_loss.cu; this
+// the kernels of the other .cu files; this
 // file only checks, describes and launches.
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -537,6 +537,7 @@ dsa_status run_kv4(const dsa_kv4_cache* c, const void* in, void* out, int L, con
   if (L <= 0 || (!in && !out) || !aligned16(in) || !aligned16(out) || !aligned16(start)) return DSA_ERR_INVALID_ARG;
   if ((long long)c->B * L >= (1LL << 31)) return DSA_ERR_UNSUPPORTED;
   Kv4Params p{};
+  p.div_l = fast_div((uint32_t)L);
   p.B = c->B; p.L = L; p.Lk = c->Lk; p.d_qk = c->d_qk; p.d_v = c->d_v;
   p.offset = offset;
   p.start = start;
@@ -900,6 +901,6 @@ dsa_status dsa_selftest_wait_timeout(uint32_t spin_limit, void* stream) {
   return v == DEV_ERR_TIMEOUT ? DSA_ERR_TIMEOUT : DSA_OK;
 }
 
-int dsa_version(void) { return 100; }
+int dsa_version(void) { return 200; }
 
 }  // extern "C"

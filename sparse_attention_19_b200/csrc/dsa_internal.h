@@ -194,6 +194,7 @@ cudaError_t launch_norm_rope_bwd(NormRopeParams p, int sms, cudaStream_t stream)
 
 // ---------------------------------------------------------------- 4-bit latent cache
 struct Kv4Params {
+  FastDiv div_l;          // by L
   int B, L, Lk, d_qk, d_v;
   int offset;             // cache row of row 0 when start is null
   const int32_t* start;   // [B] or null

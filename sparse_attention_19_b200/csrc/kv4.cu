@@ -43,8 +43,9 @@ struct Share {
   static constexpr int kRows = kThreads / kLanes;     // rows per block
 };
 
-// Cache row of input row (b, i), or -1 when it lies outside the cache.
-__device__ __forceinline__ long long cache_row(const Kv4Params& p, int b, int i) {
+// Cache row of input row `row`, or -1 when it lies outside the cache.
+__device__ __forceinline__ long long cache_row(const Kv4Params& p, int row) {
+  const int b = p.div_l(row), i = row - b * p.L;
   const long long r = (long long)(p.start ? __ldg(p.start + b) : p.offset) + i;
   return r >= 0 && r < p.Lk ? (long long)b * p.Lk + r : -1;
 }
@@ -57,7 +58,7 @@ __global__ void __launch_bounds__(kThreads) kv4_write_kernel(const Kv4Params p) 
   griddep_launch_dependents();
   griddep_wait();
   const bool here = row < p.B * p.L;
-  const long long at = here ? cache_row(p, row / p.L, row % p.L) : -1;
+  const long long at = here ? cache_row(p, row) : -1;
   const uint4* src = reinterpret_cast<const uint4*>(p.in + (size_t)(here ? row : 0) * p.d_qk);
   uint4 v[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)}, t = v[0];
   const int tail8 = (p.d_qk - DV) / 8;                // 16-byte vectors of the tail
@@ -67,12 +68,11 @@ __global__ void __launch_bounds__(kThreads) kv4_write_kernel(const Kv4Params p) 
     if (lane < tail8) t = __ldg(src + DV / 8 + lane);
   }
   const uint32_t w[8] = {v[0].x, v[0].y, v[0].z, v[0].w, v[1].x, v[1].y, v[1].z, v[1].w};
-  float x[16];
+  float2 x[8];
   uint32_t m = 0;                                     // largest magnitude as an integer: a NaN wins
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    x[2 * i] = __uint_as_float(w[i] << 16);
-    x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    x[i] = make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
     m = max(m, max((w[i] << 16) & 0x7fffffffu, w[i] & 0x7fff0000u));
   }
   m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));     // the group's other 16 columns
@@ -86,16 +86,18 @@ __global__ void __launch_bounds__(kThreads) kv4_write_kernel(const Kv4Params p) 
     // by the residual (exact in a fused multiply-add), which rounds it correctly: a value
     // halfway between two codes stays there.  Adding 1.5 * 2^23 + 8 then rounds it to
     // the nearest integer, ties to even, and leaves q + 8 in the sum's low bits.
-    const float inv = __frcp_rn(step);
+    const float r = __frcp_rn(step);
+    const float2 inv = make_float2(r, r), neg = make_float2(-step, -step);
+    const float2 magic = make_float2(12582920.f, 12582920.f);
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
       code[k] = 0;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float v = x[8 * k + e], q0 = v * inv;
-        const float q = fmaf(fmaf(-q0, step, v), inv, q0);
-        const uint32_t n = __float_as_uint(q + 12582920.f) & 15u;
-        code[k] |= n << (4 * (e / 2 + 4 * (e % 2)));
+      for (int i = 0; i < 4; ++i) {                   // columns 2i and 2i + 1: nibbles i and i + 4
+        const float2 v = x[4 * k + i], q0 = fmul2(v, inv);
+        const float2 n = fadd2(ffma2(ffma2(q0, neg, v), inv, q0), magic);
+        const uint32_t both = (__float_as_uint(n.x) & 15u) | ((__float_as_uint(n.y) & 15u) << 16);
+        code[k] |= both << (4 * i);
       }
     }
   }
@@ -107,29 +109,42 @@ __global__ void __launch_bounds__(kThreads) kv4_write_kernel(const Kv4Params p) 
   if (lane < tail8) reinterpret_cast<uint4*>(p.tail + (size_t)at * (p.d_qk - DV))[lane] = t;
 }
 
+// A thread has its share of two rows in flight (one: 13.5 us for 32768 rows, waiting for loads).
+constexpr int kReadRows = 2;
 template <int DV>
 __global__ void __launch_bounds__(kThreads) kv4_read_kernel(const Kv4Params p) {
   using S = Share<DV>;
   const int lane = threadIdx.x % S::kLanes;
-  const int row = (int)blockIdx.x * S::kRows + threadIdx.x / S::kLanes;
+  const int row0 = (int)blockIdx.x * S::kRows * kReadRows + threadIdx.x / S::kLanes;
   griddep_launch_dependents();
   griddep_wait();
-  if (row >= p.B * p.L) return;
-  const long long at = cache_row(p, row / p.L, row % p.L);
-  const int tail8 = (p.d_qk - DV) / 8, c = lane / 4, part = lane % 4;
-  uint4 v[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)}, t = v[0];
-  if (at >= 0) {
-    const uint2 code = __ldg(reinterpret_cast<const uint2*>(p.codes + (size_t)at * (DV / 2) + part * (DV / 8) + c * 8));
-    const Kv4Step step = kv4_step(reinterpret_cast<const unsigned short*>(
-        p.scales)[(size_t)at * (DV / 32) + (part / 2) * (DV / 64) + c]);
-    if (lane < tail8) t = __ldg(reinterpret_cast<const uint4*>(p.tail + (size_t)at * (p.d_qk - DV)) + lane);
-    v[0] = unpack_codes(code.x, step);
-    v[1] = unpack_codes(code.y, step);
+  const int tail8 = (p.d_qk - DV) / 8, c = lane / 4, part = lane % 4, n = p.B * p.L;
+  uint2 code[kReadRows];
+  uint32_t step[kReadRows];
+  uint4 t[kReadRows];
+#pragma unroll
+  for (int i = 0; i < kReadRows; ++i) {
+    const int row = row0 + i * S::kRows;
+    const long long at = row < n ? cache_row(p, row) : -1;
+    code[i] = make_uint2(0, 0);
+    step[i] = 0;                                      // a step of 0: zeros
+    t[i] = make_uint4(0, 0, 0, 0);
+    if (at >= 0) {
+      code[i] = __ldg(reinterpret_cast<const uint2*>(p.codes + (size_t)at * (DV / 2) + part * (DV / 8) + c * 8));
+      step[i] = reinterpret_cast<const unsigned short*>(p.scales)[(size_t)at * (DV / 32) + (part / 2) * (DV / 64) + c];
+      if (lane < tail8) t[i] = __ldg(reinterpret_cast<const uint4*>(p.tail + (size_t)at * (p.d_qk - DV)) + lane);
+    }
   }
-  uint4* dst = reinterpret_cast<uint4*>(p.out + (size_t)row * p.d_qk);
-  dst[2 * lane] = v[0];
-  dst[2 * lane + 1] = v[1];
-  if (lane < tail8) dst[DV / 8 + lane] = t;
+#pragma unroll
+  for (int i = 0; i < kReadRows; ++i) {
+    const int row = row0 + i * S::kRows;
+    if (row >= n) return;
+    const Kv4Step s = kv4_step(step[i]);
+    uint4* dst = reinterpret_cast<uint4*>(p.out + (size_t)row * p.d_qk);
+    dst[2 * lane] = unpack_codes(code[i].x, s);
+    dst[2 * lane + 1] = unpack_codes(code[i].y, s);
+    if (lane < tail8) dst[DV / 8 + lane] = t[i];
+  }
 }
 
 unsigned blocks(const Kv4Params& p, int rows_per_block) {
@@ -146,8 +161,8 @@ cudaError_t launch_kv4_write(const Kv4Params& p, cudaStream_t stream) {
 
 cudaError_t launch_kv4_read(const Kv4Params& p, cudaStream_t stream) {
   if (p.d_v == 512)
-    return launch_pdl(kv4_read_kernel<512>, dim3(blocks(p, Share<512>::kRows)), dim3(kThreads), 0, stream, p);
-  return launch_pdl(kv4_read_kernel<128>, dim3(blocks(p, Share<128>::kRows)), dim3(kThreads), 0, stream, p);
+    return launch_pdl(kv4_read_kernel<512>, dim3(blocks(p, Share<512>::kRows * kReadRows)), dim3(kThreads), 0, stream, p);
+  return launch_pdl(kv4_read_kernel<128>, dim3(blocks(p, Share<128>::kRows * kReadRows)), dim3(kThreads), 0, stream, p);
 }
 
 }  // namespace dsa

@@ -48,13 +48,6 @@ struct Vec8 {
   float2 v[4];
 };
 
-__device__ __forceinline__ float2 fmul2(float2 a, float2 b) {
-  uint64_t r;
-  asm("mul.rn.f32x2 %0, %1, %2;"
-      : "=l"(r)
-      : "l"(*reinterpret_cast<const uint64_t*>(&a)), "l"(*reinterpret_cast<const uint64_t*>(&b)));
-  return *reinterpret_cast<const float2*>(&r);
-}
 __device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
 
 // max(|m|, |x|, |y|), NaN if one of them is.

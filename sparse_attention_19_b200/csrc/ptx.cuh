@@ -230,6 +230,14 @@ __device__ __forceinline__ float2 fadd2(float2 a, float2 b) {
       : "l"(*reinterpret_cast<const uint64_t*>(&a)), "l"(*reinterpret_cast<const uint64_t*>(&b)));
   return *reinterpret_cast<const float2*>(&r);
 }
+// Two independent round-to-nearest products: (a.x*b.x, a.y*b.y).
+__device__ __forceinline__ float2 fmul2(float2 a, float2 b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;"
+      : "=l"(r)
+      : "l"(*reinterpret_cast<const uint64_t*>(&a)), "l"(*reinterpret_cast<const uint64_t*>(&b)));
+  return *reinterpret_cast<const float2*>(&r);
+}
 // 2^x by the hardware approximation (one special-function-unit instruction;
 // subnormal results flush to zero, 2^-inf = 0).
 __device__ __forceinline__ float ex2_approx(float x) {

@@ -42,6 +42,19 @@
 // = warp), warp 4 TMEM owner + S issuer (leader), warp 5 P.V issuer (leader),
 // warps 6-14 key loaders, warps 15-23 value loaders + index staging.  The softmax
 // warpgroup holds 120 registers per thread, the others 72 (setmaxnreg).
+//
+// The kernel has two more forms that differ in where the keys come from (AttnMode below):
+//   * a sliding window and sinks (kWindow): the slots of a row are computed, not listed; 16
+//     slots that are consecutive rows come in one box (72 TMA requests a tile instead of 272), a group
+//     with the seam or the end of the row by gathers.  Rows past the query or between the sinks
+//     and the window are never loaded, since a zero probability times a NaN would still
+//     reach the output.  4096 rows x (512 + 16) slots 735 us (819 TFLOP/s on the slots, 0.50 of the
+//     bf16 peak); bound by the chain S -> softmax -> P.V over only five tiles per row, the
+//     last of them one eighth full.
+//   * rows of the 4-bit cache (kPacked): 16 warps convert codes to bf16 planes in shared
+//     memory, in the layouts TMA writes for bf16 rows, once as key chunks and once as
+//     value stages.  Everything behind the operands is shared, so the result equals the bf16
+//     kernel's over the values that the cache holds bit for bit.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
