@@ -390,17 +390,17 @@ def _need_at(t, dtype, shape, name, device):
         raise ValueError(f"{name} is on {t.device}, expected {device}")
 
 
-def _on(device, stream, call):
-    """call(stream handle) with `device` current, and with what it allocates belonging to
+def _on(device, stream, call, *args):
+    """call(stream handle, *args) with `device` current, and with what it allocates belonging to
     the stream that it launches on (a workspace freed on return is then reused in that
     stream's order)."""
     if stream is None and device.index == torch.cuda.current_device():
-        return call(torch._C._cuda_getCurrentRawStream(device.index))   # as an integer: a Stream object costs 3 us
+        return call(torch._C._cuda_getCurrentRawStream(device.index), *args)   # an integer: a Stream object costs 3 us
     if stream is not None and stream.device != device:
         raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
     with torch.cuda.device(device):
         with torch.cuda.stream(stream if stream is not None else torch.cuda.current_stream(device)):
-            return call(ctypes.c_void_p(torch.cuda.current_stream().cuda_stream))
+            return call(torch.cuda.current_stream().cuda_stream, *args)
 
 
 def _need_workspace(ws, device):
@@ -534,11 +534,11 @@ def kv4_cache(B, Lk, d_qk, d_v, device="cuda"):
 
 
 def _kv4(codes, scales, tail):
-    if not isinstance(codes, torch.Tensor) or codes.dim() != 3:
-        raise ValueError("codes must be a torch.Tensor [B, Lk, d_v/2]")
+    if not isinstance(codes, torch.Tensor) or codes.dim() != 3 or not codes.is_cuda:
+        raise ValueError("codes must be a CUDA tensor [B, Lk, d_v/2]")
     B, Lk, half = codes.shape
     dev = codes.device
-    _need(codes, torch.uint8, (B, Lk, half), "codes")
+    _need_at(codes, torch.uint8, (B, Lk, half), "codes", dev)
     _need_at(scales, torch.bfloat16, (B, Lk, half // 16), "scales", dev)
     _need_at(tail, torch.bfloat16, (B, Lk, tail.shape[-1]), "tail", dev)
     return Kv4Cache(B, Lk, 2 * half + tail.shape[-1], 2 * half, codes.data_ptr(), scales.data_ptr(), tail.data_ptr())
@@ -554,8 +554,13 @@ def kv4_write(kv, codes, scales, tail, start=None, offset=0, stream=None):
     _need_at(kv, torch.bfloat16, (c.B, L, c.d_qk), "kv", dev)
     if start is not None:
         _need_at(start, torch.int32, (c.B,), "start", dev)
-    _on(dev, stream, lambda st: _check(lib().dsa_kv4_write(ctypes.byref(c), kv.data_ptr(), L, _ptr(start),
-                                                           int(offset), st), "dsa_kv4_write"))
+    _on(dev, stream, _kv4_write, c, kv, L, None if start is None else start.data_ptr(), int(offset))
+
+
+def _kv4_write(st, c, kv, L, start, offset):
+    rc = lib().dsa_kv4_write(ctypes.byref(c), kv.data_ptr(), L, start, offset, st)
+    if rc:
+        raise DSAError(rc, "dsa_kv4_write")
 
 
 def kv4_read(codes, scales, tail, L, start=None, offset=0, kv=None, stream=None):
@@ -570,10 +575,11 @@ def kv4_read(codes, scales, tail, L, start=None, offset=0, kv=None, stream=None)
     def call(st):
         o = kv
         if o is None:
-            o = torch.empty((c.B, L, c.d_qk), dtype=torch.bfloat16, device=dev)
+            o = tail.new_empty((c.B, L, c.d_qk))
         else:
             _need_at(o, torch.bfloat16, (c.B, L, c.d_qk), "kv", dev)
-        _check(lib().dsa_kv4_read(ctypes.byref(c), o.data_ptr(), L, _ptr(start), int(offset), st), "dsa_kv4_read")
+        _check(lib().dsa_kv4_read(ctypes.byref(c), o.data_ptr(), L, None if start is None else start.data_ptr(),
+                                  int(offset), st), "dsa_kv4_read")
         return o
 
     return _on(dev, stream, call)
@@ -581,20 +587,21 @@ def kv4_read(codes, scales, tail, L, start=None, offset=0, kv=None, stream=None)
 
 def _kv4_attn_args(q, codes, scales, tail, scale):
     c = _kv4(codes, scales, tail)
-    B, Lq, H, D = q.shape
+    _, Lq, H, _ = q.shape
     _need_at(q, torch.bfloat16, (c.B, Lq, H, c.d_qk), "q", codes.device)
-    return c, Kv4AttnArgs(H, c.d_qk, c.d_v, float(scale), q.data_ptr(), c.codes, c.scales, c.tail)
+    return c, Kv4AttnArgs(H, c.d_qk, c.d_v, scale, q.data_ptr(), c.codes, c.scales, c.tail)
 
 
-def _attn_outputs(B, Lq, H, d_v, out, lse, want_lse, device):
+def _attn_outputs(q, d_v, out, lse, want_lse):
+    B, Lq, H, _ = q.shape
     if out is None:
-        out = torch.empty(B, Lq, H, d_v, dtype=torch.bfloat16, device=device)
+        out = q.new_empty((B, Lq, H, d_v))
     else:
-        _need_at(out, torch.bfloat16, (B, Lq, H, d_v), "out", device)
+        _need_at(out, torch.bfloat16, (B, Lq, H, d_v), "out", q.device)
     if lse is None and want_lse:
-        lse = torch.empty(B, Lq, H, dtype=torch.float32, device=device)
+        lse = torch.empty((B, Lq, H), dtype=torch.float32, device=q.device)
     elif lse is not None:
-        _need_at(lse, torch.float32, (B, Lq, H), "lse", device)
+        _need_at(lse, torch.float32, (B, Lq, H), "lse", q.device)
     return out, lse
 
 
@@ -608,10 +615,10 @@ def sparse_attn_kv4(q, codes, scales, tail, indices, scale, out=None, lse=None, 
     _need_workspace(workspace, dev)
 
     def call(st):
-        o, l = _attn_outputs(c.B, Lq, a.H, c.d_v, out, lse, want_lse, dev)
+        o, l = _attn_outputs(q, c.d_v, out, lse, want_lse)
         ws, nbytes = _workspace(OP_SPARSE_ATTN, c.B, Lq, max(c.Lk, Lq), k, a.H, c.d_v, dev, workspace)
-        _check(lib().dsa_sparse_attn_kv4(ctypes.byref(a), c.B, Lq, c.Lk, _ptr(indices), k, _ptr(o), _ptr(l), _ptr(ws),
-                                         nbytes, st), "dsa_sparse_attn_kv4")
+        _check(lib().dsa_sparse_attn_kv4(ctypes.byref(a), c.B, Lq, c.Lk, indices.data_ptr(), k, o.data_ptr(), _ptr(l),
+                                         _ptr(ws), nbytes, st), "dsa_sparse_attn_kv4")
         return o, l
 
     return _on(dev, stream, call)
@@ -635,7 +642,7 @@ def forward_kv4(q_I, q_scale, w, k_I, k_scale, q, codes, scales, tail, k, scale,
     def call(st):
         i = torch.empty(ia.B, ia.Lq, k, dtype=torch.int32, device=dev) if indices is None else indices
         _need_at(i, torch.int32, (ia.B, ia.Lq, k), "indices", dev)
-        o, l = _attn_outputs(ia.B, ia.Lq, a.H, c.d_v, out, lse, want_lse, dev)
+        o, l = _attn_outputs(q, c.d_v, out, lse, want_lse)
         ws, nbytes = _workspace(OP_FORWARD_LOWMEM if low_memory else OP_FORWARD, ia.B, ia.Lq, ia.Lk, k, a.H, c.d_v,
                                 dev, workspace, ia=ia)
         _check(lib().dsa_forward_kv4(ctypes.byref(ia), ctypes.byref(a), int(k), _ptr(i), _ptr(sel_scores), _ptr(o),
@@ -663,7 +670,7 @@ def window_attn(q, kv, d_v, scale, window, sinks=0, q_offset=0, start=None, out=
     window, sinks = min(int(window), 2 ** 31 - 1), min(int(sinks), 2 ** 31 - 1)
 
     def call(st):
-        o, l = _attn_outputs(B, Lq, H, int(d_v), out, lse, want_lse, dev)
+        o, l = _attn_outputs(q, int(d_v), out, lse, want_lse)
         ws, nbytes = _workspace(OP_WINDOW_ATTN, B, Lq, Lk, min(window + sinks, Lk), H, int(d_v), dev, workspace)
         _check(lib().dsa_window_attn(ctypes.byref(a), B, Lq, Lk, int(q_offset), _ptr(start), window, sinks, _ptr(o),
                                      _ptr(l), _ptr(ws), nbytes, st), "dsa_window_attn")

@@ -59,6 +59,7 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cstdint>
 
 #include "dsa_internal.h"
@@ -1148,11 +1149,18 @@ cudaError_t launch_t(const AttnParams& p, const CUtensorMap& tq, const CUtensorM
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
   // The register split must fit in what the CTA launches with, or the increase
-  // would wait forever: refuse to launch a build where it does not.
-  cudaFuncAttributes fa;
-  e = cudaFuncGetAttributes(&fa, kern);
-  if (e != cudaSuccess) return e;
-  if (C::kSplitRegs && (uint32_t)fa.numRegs < kRegsLaunch) return cudaErrorInvalidConfiguration;
+  // would wait forever: refuse to launch a build where it does not.  (A property of
+  // the binary: asked for once.)
+  if constexpr (C::kSplitRegs) {
+    static std::atomic<bool> fits{false};
+    if (!fits.load(std::memory_order_relaxed)) {
+      cudaFuncAttributes fa;
+      e = cudaFuncGetAttributes(&fa, kern);
+      if (e != cudaSuccess) return e;
+      if ((uint32_t)fa.numRegs < kRegsLaunch) return cudaErrorInvalidConfiguration;
+      fits.store(true, std::memory_order_relaxed);
+    }
+  }
   return launch_pdl(kern, dim3(grid_clusters * 2), dim3(C::kThreads), smem, stream, tq, tkv, tkv_tile, p);
 }
 
