@@ -42,6 +42,8 @@ constexpr int kThreads = 256;
 // Blocks of an SM that the registers of the bf16 kernel are to allow: more rows in flight for
 // rows of few slots (the layer norm's second sum would spill there), fewer for rows of many.
 constexpr int resident(int slots, bool layer) { return slots > 6 ? 1 : slots > 4 || layer ? 2 : 3; }
+// The same for the e4m3 kernel, whose barrier per step other blocks have to fill.
+constexpr int resident_e4m3(int slots, bool layer) { return slots > 6 ? 1 : slots > 4 ? 2 : layer ? 3 : 4; }
 constexpr float kAmaxFloor = 1e-30f;           // an all-zero token keeps a positive scale
 
 struct Vec8 {
@@ -98,7 +100,7 @@ __device__ __forceinline__ float group_sum(float x) {
 // Without a rotation the "range" is the row's first vectors, so that no slot is wasted.
 // FULL rows fill every slot of every lane, the rotated range lies at one end of the row and
 // the norm covers all or none of it and of the rest: then nothing is checked per vector
-// (8K indexer queries to e4m3: 57 us with the checks, see the launch for the time without).
+// (8192 x 64 x 128 to e4m3: 57 us with the checks, 53 without).
 template <int G, int NP, int NM, bool FULL>
 struct Slots {
   static constexpr int kN = 2 * NP + NM;
@@ -321,7 +323,8 @@ __device__ __forceinline__ uint2 to_e4m3(const Vec8& y, float2 inv) {
 __device__ __forceinline__ float inv_scale(float amax) { return 1.f / (amax * (1.f / 448.f)); }
 
 // bf16 output.  Persistent blocks; while a step is computed the next one's rows are in
-// flight, and one barrier per span completes its angles.
+// flight, and one barrier per span completes its angles.  Bound by HBM: 0.86-0.90 of the copy
+// rate at 4096 x 128 x 192 (72 us; one step per block and nothing in flight behind it 147 us).
 template <int G, int NP, int NM, bool FULL, bool LAYER>
 __global__ void __launch_bounds__(kThreads, resident(2 * NP + NM, LAYER)) norm_rope_kernel(const NormRopeParams p) {
   using S = Slots<G, NP, NM, FULL>;
@@ -386,11 +389,14 @@ __global__ void __launch_bounds__(kThreads, resident(2 * NP + NM, LAYER)) norm_r
   }
 }
 
-// e4m3 output.  A step holds whole tokens, R rows per group of lanes in registers (so that the
-// weights are read once for R rows, and the one barrier a step needs for its tokens'
-// maxima serves R times the rows).
-template <int G, int NP, int NM, bool FULL, int R, bool LAYER>
-__global__ void __launch_bounds__(kThreads, 2 * NP + NM > 6 ? 1 : R > 1 || 2 * NP + NM > 4 ? 2 : LAYER ? 3 : 4) norm_rope_e4m3_kernel(const NormRopeParams p) {
+// e4m3 output.  A step holds whole tokens, a row per group of lanes in registers; its one
+// barrier completes the tokens' maxima.  Bound by issue slots (62 %) and the load/store pipe
+// (60 %) alike, 0.64 of the copy rate at 8192 x 64 x 128 (48 us): weights and angles come
+// from shared memory for every row, since holding them in registers costs more in warps (53
+// registers: four blocks an SM; the weights in registers 63-70 us, two rows per group with
+// one weight read 64 us, five blocks 54 us).
+template <int G, int NP, int NM, bool FULL, bool LAYER>
+__global__ void __launch_bounds__(kThreads, resident_e4m3(2 * NP + NM, LAYER)) norm_rope_e4m3_kernel(const NormRopeParams p) {
   using S = Slots<G, NP, NM, FULL>;
   constexpr int N = S::kN, kGroups = kThreads / G;
   extern __shared__ __align__(16) float smem[];
@@ -398,12 +404,7 @@ __global__ void __launch_bounds__(kThreads, 2 * NP + NM > 6 ? 1 : R > 1 || 2 * N
   float* w = smem + 4 * table;                           // behind two buffers of cos and sin
   float* amax3 = w + p.norm_dim * (p.b ? 2 : 1);         // three buffers of one value per token
   const int lane = threadIdx.x % G, group = threadIdx.x / G;
-  int tl_group[R], h_group[R];
-#pragma unroll
-  for (int i = 0; i < R; ++i) {
-    tl_group[i] = p.div_h(i * kGroups + group);
-    h_group[i] = i * kGroups + group - tl_group[i] * p.H;
-  }
+  const int tl_group = p.div_h(group), h_group = group - tl_group * p.H;
   const S slots(p, lane);
   griddep_launch_dependents();
   griddep_wait();
@@ -415,68 +416,52 @@ __global__ void __launch_bounds__(kThreads, 2 * NP + NM > 6 ? 1 : R > 1 || 2 * N
     q.enter(p, span);
     const float* cs0 = smem + buf * 2 * table;
     for (; q.step < q.steps; ++q.step) {
-      Row r[R];
-      uint4 raw[R][N];
+      const Row r = q.row(p, tl_group, h_group, 0, kGroups);
+      const uint4* src = r.source(p);
+      uint4 raw[N];
 #pragma unroll
-      for (int i = 0; i < R; ++i) {
-        r[i] = q.row(p, tl_group[i], h_group[i], 0, 0);
-        const uint4* src = r[i].source(p);
-#pragma unroll
-        for (int n = 0; n < N; ++n)
-          raw[i][n] = slots.load(src, n, r[i].here);
-      }
+      for (int n = 0; n < N; ++n) raw[n] = slots.load(src, n, r.here);
       if (q.step == 0) {
         if (p.n_freq) fill_angles(p, q.tok0, q.ntok, smem + buf * 2 * table, smem + buf * 2 * table + table);
         __syncthreads();
       }
-      Vec8 y[R][N];
+      Vec8 y[N];
 #pragma unroll
-      for (int i = 0; i < R; ++i) {
+      for (int n = 0; n < N; ++n) y[n] = unpack8(raw[n]);
+      normalise<G, LAYER>(p, y, slots);
 #pragma unroll
-        for (int n = 0; n < N; ++n) y[i][n] = unpack8(raw[i][n]);
-        normalise<G, LAYER>(p, y[i], slots);
-      }
+      for (int n = 0; n < N; ++n) scale8<LAYER>(p, y[n], slots, n, w);
+      const float* cs = cs0 + (r.tok - q.tok0) * p.n_freq;
+      if (p.n_freq)
 #pragma unroll
-      for (int n = 0; n < N; ++n)
-#pragma unroll
-        for (int i = 0; i < R; ++i) scale8<LAYER>(p, y[i][n], slots, n, w);
+        for (int n = 0; n < NP; ++n)
+          if (slots.has(2 * n)) rotate_pair(p, n * G + lane, y[2 * n], y[2 * n + 1], cs, cs + table, 1.f);
       float* amax = amax3 + a3 * p.tokens_per_step;
       a3 = a3 == 2 ? 0 : a3 + 1;
       float* amax_next = amax3 + a3 * p.tokens_per_step;
       const int first = q.tok0 + q.first(p);
+      // The maximum does not depend on the order, and a NaN wins (also as an integer).
+      float m = 0.f;
 #pragma unroll
-      for (int i = 0; i < R; ++i) {
-        const float* cs = cs0 + (r[i].tok - q.tok0) * p.n_freq;
-        if (p.n_freq)
+      for (int n = 0; n < N; ++n)
 #pragma unroll
-          for (int n = 0; n < NP; ++n)
-            if (slots.has(2 * n)) rotate_pair(p, n * G + lane, y[i][2 * n], y[i][2 * n + 1], cs, cs + table, 1.f);
-        // The maximum does not depend on the order, and a NaN wins (also as an integer).
-        float m = 0.f;
+        for (int e = 0; e < 4; ++e) m = max_abs(m, y[n].v[e].x, y[n].v[e].y);
+      if (!r.here) m = 0.f;
+      const bool one = p.H % (32 / G) == 0;              // every row of the warp is of one token
 #pragma unroll
-        for (int n = 0; n < N; ++n)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) m = max_abs(m, y[i][n].v[e].x, y[i][n].v[e].y);
-        if (!r[i].here) m = 0.f;
-        const bool one = p.H % (32 / G) == 0;            // every row of the warp is of one token
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1)
-          if (o < G || one) m = max_abs(m, __shfl_xor_sync(0xffffffffu, m, o), 0.f);
-        if ((one ? threadIdx.x % 32 : lane) == 0 && r[i].here)
-          atomicMax(reinterpret_cast<int*>(&amax[r[i].tok - first]), __float_as_int(m));
-      }
+      for (int o = 16; o > 0; o >>= 1)
+        if (o < G || one) m = max_abs(m, __shfl_xor_sync(0xffffffffu, m, o), 0.f);
+      if ((one ? threadIdx.x % 32 : lane) == 0 && r.here)
+        atomicMax(reinterpret_cast<int*>(&amax[r.tok - first]), __float_as_int(m));
       for (int t = threadIdx.x; t < p.tokens_per_step; t += kThreads) amax_next[t] = kAmaxFloor;
       __syncthreads();
       if (threadIdx.x < q.count(p)) p.scale[first + threadIdx.x] = amax[threadIdx.x] / 448.f;
+      if (!r.here) continue;
+      const float2 inv = both(inv_scale(amax[r.tok - first]));
+      uint2* dst = reinterpret_cast<uint2*>(p.codes) + r.offset(p);
 #pragma unroll
-      for (int i = 0; i < R; ++i) {
-        if (!r[i].here) continue;
-        const float2 inv = both(inv_scale(amax[r[i].tok - first]));
-        uint2* dst = reinterpret_cast<uint2*>(p.codes) + r[i].offset(p);
-#pragma unroll
-        for (int n = 0; n < N; ++n)
-          if (slots.has(n)) dst[slots.vec(n)] = to_e4m3(y[i][n], inv);
-      }
+      for (int n = 0; n < N; ++n)
+        if (slots.has(n)) dst[slots.vec(n)] = to_e4m3(y[n], inv);
     }
   }
 }
@@ -543,7 +528,9 @@ __global__ void __launch_bounds__(kThreads) norm_rope_wide_kernel(const NormRope
 
 // Gradient.  Each block keeps the sums for dw and db of its columns in registers over all its
 // steps and leaves one partial row; a second kernel adds the partial rows in block
-// order, so the result does not depend on timing.
+// order, so the result does not depend on timing.  0.73 of the copy rate at 4096 x 64 x 128 (42
+// us): the running sums take registers (127), so 16 warps an SM have to cover the loads.  Two
+// blocks an SM in one wave: twice as many blocks in two waves took 47 us.
 template <int G, int NP, int NM, bool FULL, bool LAYER>
 __global__ void __launch_bounds__(kThreads, (2 * NP + NM) > 4 ? 1 : 2) norm_rope_bwd_kernel(const NormRopeParams p) {
   using S = Slots<G, NP, NM, FULL>;
@@ -711,16 +698,16 @@ cudaError_t by_width(const NormRopeParams& p, Fn&& f) {
   return cudaErrorInvalidValue;
 }
 
-// Steps and spans for blocks of `groups` groups that hold `rows` rows a step; returns the grid.
+// Steps and spans for blocks of `groups` rows a step; returns the grid.
 //   step: as many whole tokens as a block holds, but with few tokens only as many as spread
 //         them over the SMs; or part of a token's heads when a block holds less than one;
 //   span: a block's even share of the tokens, or an even part of it when the angles of the
 //         share would take more than 16 KB.
-unsigned plan_walk(NormRopeParams& p, int groups, int rows, int sms, int blocks) {
+unsigned plan_walk(NormRopeParams& p, int groups, int sms, int blocks) {
   const long long n = p.n_tokens;
-  p.parts = p.H <= rows ? 1 : (p.H + groups - 1) / groups;
+  p.parts = (p.H + groups - 1) / groups;
   p.div_parts = fast_div((uint32_t)p.parts);
-  long long t = rows / p.H;
+  long long t = groups / p.H;
   const long long spread = (n + 2 * sms - 1) / (2 * sms);
   if (t > spread) t = spread;
   const long long table = p.n_freq ? 16384 / (8LL * p.n_freq) : t;
@@ -746,18 +733,17 @@ cudaError_t launch_norm_rope(NormRopeParams p, int sms, cudaStream_t stream) {
     const size_t params = (size_t)p.norm_dim * (p.b ? 2 : 1);
     constexpr int kGroups = kThreads / G;
     if (!p.codes) {
-      const unsigned grid = plan_walk(p, kGroups, kGroups, sms, sms * resident(2 * NP + NM, layer));
+      const unsigned grid = plan_walk(p, kGroups, sms, sms * resident(2 * NP + NM, layer));
       const size_t smem = ((size_t)p.span_tokens * p.n_freq * 4 + params) * sizeof(float);
       return launch_pdl(layer ? norm_rope_kernel<G, NP, NM, FULL, true> : norm_rope_kernel<G, NP, NM, FULL, false>, dim3(grid),
                         dim3(kThreads), smem, stream, p);
     }
-    constexpr int R = 1;
-    if (p.H > R * kGroups)
+    if (p.H > kGroups)
       return launch_pdl(layer ? norm_rope_wide_kernel<G, NP, NM, true> : norm_rope_wide_kernel<G, NP, NM, false>,
                         dim3(p.n_tokens), dim3(kThreads), (2 * p.n_freq + params) * sizeof(float), stream, p);
-    const unsigned grid = plan_walk(p, kGroups, R * kGroups, sms, sms * 4);
+    const unsigned grid = plan_walk(p, kGroups, sms, sms * resident_e4m3(2 * NP + NM, layer));
     const size_t smem = ((size_t)p.span_tokens * p.n_freq * 4 + params + 3 * p.tokens_per_step) * sizeof(float);
-    return launch_pdl(layer ? norm_rope_e4m3_kernel<G, NP, NM, FULL, R, true> : norm_rope_e4m3_kernel<G, NP, NM, FULL, R, false>,
+    return launch_pdl(layer ? norm_rope_e4m3_kernel<G, NP, NM, FULL, true> : norm_rope_e4m3_kernel<G, NP, NM, FULL, false>,
                       dim3(grid), dim3(kThreads), smem, stream, p);
   });
 }
@@ -770,7 +756,7 @@ cudaError_t launch_norm_rope_bwd(NormRopeParams p, int sms, cudaStream_t stream)
   const cudaError_t e = by_width(p, [&](auto g, auto np, auto nm, auto full) {
     constexpr int G = decltype(g)::value, NP = decltype(np)::value, NM = decltype(nm)::value;
     constexpr bool FULL = decltype(full)::value;
-    grid = (int)plan_walk(p, kThreads / G, kThreads / G, sms, norm_rope_bwd_blocks(sms));
+    grid = (int)plan_walk(p, kThreads / G, sms, norm_rope_bwd_blocks(sms));
     size_t smem = ((size_t)p.span_tokens * p.n_freq * 4 + p.norm_dim * (p.b ? 2 : 1)) * sizeof(float);
     const size_t red = (size_t)(kThreads / 32) * p.norm_dim * sizeof(float);
     if (red > smem) smem = red;
