@@ -390,6 +390,14 @@ def _need_at(t, dtype, shape, name, device):
         raise ValueError(f"{name} is on {t.device}, expected {device}")
 
 
+def _int32(v, name):
+    """v as an int that the C side's 32 bits hold (ctypes would wrap it silently)."""
+    v = int(v)
+    if not -2 ** 31 <= v < 2 ** 31:
+        raise ValueError(f"{name} {v} does not fit 32 bits")
+    return v
+
+
 def _on(device, stream, call, *args):
     """call(stream handle, *args) with `device` current, and with what it allocates belonging to
     the stream that it launches on (a workspace freed on return is then reused in that
@@ -420,6 +428,9 @@ _NORMS = {None: 0, "rms": 1, "layer": 2}
 
 
 def _norm_rope_args(x, inv_freq, weight, bias, norm, norm_dim, eps, rot_start, interleaved, positions, q_offset):
+    rot_start, q_offset = _int32(rot_start, "rot_start"), _int32(q_offset, "q_offset")
+    if norm_dim is not None:
+        norm_dim = _int32(norm_dim, "norm_dim")
     if not isinstance(x, torch.Tensor) or x.dtype != torch.bfloat16:
         raise TypeError("x must be a bfloat16 torch.Tensor")
     if x.dim() != 4:
@@ -433,7 +444,7 @@ def _norm_rope_args(x, inv_freq, weight, bias, norm, norm_dim, eps, rot_start, i
     w_ptr = b_ptr = f_ptr = pos_ptr = None
     n_freq = w_bf16 = 0
     if norm is not None:
-        norm_dim = D if norm_dim is None else int(norm_dim)
+        norm_dim = D if norm_dim is None else norm_dim
         w_bf16 = isinstance(weight, torch.Tensor) and weight.dtype is torch.bfloat16
         wt = torch.bfloat16 if w_bf16 else torch.float32
         _need_at(weight, wt, (norm_dim,), "weight", dev)
@@ -494,6 +505,8 @@ def norm_rope_bwd(dy, x, inv_freq=None, *, weight=None, bias=None, norm=None, no
                   stream=None):
     """Gradient of norm_rope's bf16 output: (dx bf16 [B, L, H, D], dweight fp32 or None,
     dbias fp32 or None) for ``dy`` bf16 [B, L, H, D]; the other arguments as in the forward."""
+    if norm is None and (dweight is not None or dbias is not None):
+        raise ValueError("dweight and dbias belong to a norm")
     a = _norm_rope_args(x, inv_freq, weight, bias, norm, norm_dim, eps, rot_start, interleaved, positions, q_offset)
     dev, shape = x.device, x.shape
     _need_at(dy, torch.bfloat16, shape, "dy", dev)
@@ -548,13 +561,14 @@ def kv4_write(kv, codes, scales, tail, start=None, offset=0, stream=None):
     """Stores latent rows ``kv`` (bf16 [B, L, d_qk]) in rows first .. first + L - 1 of each
     sequence of the 4-bit cache; first is ``start`` (int32 [B]) or ``offset``.  Rows outside
     the cache are not stored; the cache's other rows stay as they were."""
+    offset = _int32(offset, "offset")
     c = _kv4(codes, scales, tail)
     dev = codes.device
     L = kv.shape[1]
     _need_at(kv, torch.bfloat16, (c.B, L, c.d_qk), "kv", dev)
     if start is not None:
         _need_at(start, torch.int32, (c.B,), "start", dev)
-    _on(dev, stream, _kv4_write, c, kv, L, None if start is None else start.data_ptr(), int(offset))
+    _on(dev, stream, _kv4_write, c, kv, L, None if start is None else start.data_ptr(), offset)
 
 
 def _kv4_write(st, c, kv, L, start, offset):
@@ -566,9 +580,9 @@ def _kv4_write(st, c, kv, L, start, offset):
 def kv4_read(codes, scales, tail, L, start=None, offset=0, kv=None, stream=None):
     """bf16 [B, L, d_qk]: rows first .. first + L - 1 of each sequence as the values the
     4-bit cache holds (rows outside the cache: zeros)."""
+    L, offset = _int32(L, "L"), _int32(offset, "offset")
     c = _kv4(codes, scales, tail)
     dev = codes.device
-    L = int(L)
     if start is not None:
         _need_at(start, torch.int32, (c.B,), "start", dev)
 
@@ -579,7 +593,7 @@ def kv4_read(codes, scales, tail, L, start=None, offset=0, kv=None, stream=None)
         else:
             _need_at(o, torch.bfloat16, (c.B, L, c.d_qk), "kv", dev)
         _check(lib().dsa_kv4_read(ctypes.byref(c), o.data_ptr(), L, None if start is None else start.data_ptr(),
-                                  int(offset), st), "dsa_kv4_read")
+                                  offset, st), "dsa_kv4_read")
         return o
 
     return _on(dev, stream, call)
@@ -627,6 +641,7 @@ def sparse_attn_kv4(q, codes, scales, tail, indices, scale, out=None, lse=None, 
 def forward_kv4(q_I, q_scale, w, k_I, k_scale, q, codes, scales, tail, k, scale, q_offset=0, indices=None, out=None,
                 lse=None, want_lse=True, workspace=None, stream=None, sel_scores=None, low_memory=False):
     """forward with the latent rows in a 4-bit cache.  Returns (indices, out, lse)."""
+    k, q_offset = _int32(k, "k"), _int32(q_offset, "q_offset")
     c, a = _kv4_attn_args(q, codes, scales, tail, scale)
     dev = q.device
     ia = _indexer_args(q_I, q_scale, w, k_I, k_scale, q_offset)
@@ -645,7 +660,7 @@ def forward_kv4(q_I, q_scale, w, k_I, k_scale, q, codes, scales, tail, k, scale,
         o, l = _attn_outputs(q, c.d_v, out, lse, want_lse)
         ws, nbytes = _workspace(OP_FORWARD_LOWMEM if low_memory else OP_FORWARD, ia.B, ia.Lq, ia.Lk, k, a.H, c.d_v,
                                 dev, workspace, ia=ia)
-        _check(lib().dsa_forward_kv4(ctypes.byref(ia), ctypes.byref(a), int(k), _ptr(i), _ptr(sel_scores), _ptr(o),
+        _check(lib().dsa_forward_kv4(ctypes.byref(ia), ctypes.byref(a), k, _ptr(i), _ptr(sel_scores), _ptr(o),
                                      _ptr(l), _ptr(ws), nbytes, st), "dsa_forward_kv4")
         return i, o, l
 
@@ -658,6 +673,9 @@ def window_attn(q, kv, d_v, scale, window, sinks=0, q_offset=0, start=None, out=
     keys (t - window, t] and the first ``sinks`` ones: bf16 [B, Lq, H, d_v] and fp32 lse
     [B, Lq, H].  ``start``: int32 [B], any values; a query that sees nothing gets out = 0 and
     lse = -inf.  Keys that no query sees may hold anything."""
+    window = _int32(min(window, 2 ** 31 - 1), "window")     # wider than any sequence: all keys
+    sinks = _int32(min(sinks, 2 ** 31 - 1), "sinks")
+    q_offset = _int32(q_offset, "q_offset")
     a = _attn_args(q, kv, d_v, scale)
     dev = q.device
     B, Lq, H, _ = q.shape
@@ -667,12 +685,11 @@ def window_attn(q, kv, d_v, scale, window, sinks=0, q_offset=0, start=None, out=
     if start is not None:
         _need_at(start, torch.int32, (B,), "start", dev)
     _need_workspace(workspace, dev)
-    window, sinks = min(int(window), 2 ** 31 - 1), min(int(sinks), 2 ** 31 - 1)
 
     def call(st):
         o, l = _attn_outputs(q, int(d_v), out, lse, want_lse)
         ws, nbytes = _workspace(OP_WINDOW_ATTN, B, Lq, Lk, min(window + sinks, Lk), H, int(d_v), dev, workspace)
-        _check(lib().dsa_window_attn(ctypes.byref(a), B, Lq, Lk, int(q_offset), _ptr(start), window, sinks, _ptr(o),
+        _check(lib().dsa_window_attn(ctypes.byref(a), B, Lq, Lk, q_offset, _ptr(start), window, sinks, _ptr(o),
                                      _ptr(l), _ptr(ws), nbytes, st), "dsa_window_attn")
         return o, l
 

@@ -173,6 +173,41 @@ def test_binding_refuses_tensors_that_are_not_on_a_gpu():
         dsa.kv4_read(codes, scales, tail, 1)
 
 
+_X = torch.zeros(1, 4, 2, 64, dtype=torch.bfloat16)
+_Q = torch.zeros(1, 4, 2, 192, dtype=torch.bfloat16)
+_KV = torch.zeros(1, 8, 192, dtype=torch.bfloat16)
+
+
+@pytest.mark.parametrize("name,call", [
+    ("q_offset", lambda v: dsa.norm_rope(_X, q_offset=v)),
+    ("rot_start", lambda v: dsa.norm_rope(_X, rot_start=v)),
+    ("norm_dim", lambda v: dsa.norm_rope(_X, norm="rms", norm_dim=v)),
+    ("q_offset", lambda v: dsa.norm_rope_bwd(_X, _X, q_offset=v)),
+    ("offset", lambda v: dsa.kv4_write(_KV, *dsa.kv4_cache(1, 8, 192, 128, device="cpu"), offset=v)),
+    ("offset", lambda v: dsa.kv4_read(*dsa.kv4_cache(1, 8, 192, 128, device="cpu"), 4, offset=v)),
+    ("L", lambda v: dsa.kv4_read(*dsa.kv4_cache(1, 8, 192, 128, device="cpu"), v)),
+    ("q_offset", lambda v: dsa.window_attn(_Q, _KV, 128, 1.0, 4, q_offset=v)),
+])
+@pytest.mark.parametrize("value", [2 ** 31, 2 ** 32, -2 ** 31 - 1, -2 ** 32])
+def test_binding_refuses_integers_beyond_32_bits(name, call, value):
+    """The C side takes 32-bit integers; a wrapped one would name another row or position."""
+    with pytest.raises(ValueError, match=f"{name}.* 32 bits"):
+        call(value)
+
+
+@pytest.mark.parametrize("kw", [dict(window=-2 ** 32 + 5), dict(window=4, sinks=-2 ** 32)])
+def test_binding_refuses_windows_far_below_zero(kw):
+    with pytest.raises(ValueError, match="32 bits"):
+        dsa.window_attn(_Q, _KV, 128, 1.0, **kw)
+
+
+@pytest.mark.parametrize("name", ["dweight", "dbias"])
+def test_binding_refuses_gradients_of_a_norm_that_is_not_there(name):
+    """They would come back as they were given."""
+    with pytest.raises(ValueError, match="belong to a norm"):
+        dsa.norm_rope_bwd(_X, _X, **{name: torch.zeros(64)})
+
+
 @pytest.mark.parametrize("kind", ["rms", "layer", None])
 @pytest.mark.parametrize("interleaved", [False, True])
 def test_gradient_form_against_differences(kind, interleaved):
