@@ -76,7 +76,9 @@ typedef enum {
     DSA_OP_FORWARD = 2,          /* dsa_forward, staged selection (the faster path) */
     DSA_OP_INDEXER_TOPK = 3,
     DSA_OP_FORWARD_LOWMEM = 4,   /* dsa_forward, fused selection (no score matrix) */
-    DSA_OP_WINDOW_ATTN = 5       /* dsa_window_attn; k = window + sinks (of any size) */
+    DSA_OP_WINDOW_ATTN = 5,      /* dsa_window_attn; k = window + sinks (of any size) */
+    DSA_OP_SPARSE_ATTN_KV4 = 6,  /* dsa_sparse_attn_kv4 with room to unpack the cache where that is faster */
+    DSA_OP_FORWARD_KV4 = 7       /* dsa_forward_kv4, staged selection and the same room */
 } dsa_op;
 
 /*
@@ -338,8 +340,12 @@ dsa_status dsa_kv4_read(const dsa_kv4_cache *cache, void *kv, int L, const int32
 /*
  * dsa_sparse_attn over the 4-bit cache: the same attention with c_s as the cache holds it
  * (its values are exact in bf16, so nothing is rounded on the way to the matrix product).
- *   indices, k, out, lse, workspace (DSA_OP_SPARSE_ATTN), limits: as dsa_sparse_attn.  Rows of
- *   the cache that no valid entry names are not read, so they may hold anything.
+ *   indices, k, out, lse, limits: as dsa_sparse_attn.  Rows of the cache that no valid entry
+ *   of a query names have no part in its result: they may hold anything.
+ *   workspace: DSA_OP_SPARSE_ATTN bytes at least.  Where the lists name each row many times (a
+ *   prefill chunk) DSA_OP_SPARSE_ATTN_KV4 asks for room for the rows in bf16 as well
+ *   (B * Lk * d_qk * 2 bytes, for the call only); with it the cache is unpacked once instead
+ *   of at every use.  The result is the same bit for bit.
  */
 typedef struct {
     int H, d_qk, d_v;
@@ -353,7 +359,8 @@ dsa_status dsa_sparse_attn_kv4(const dsa_kv4_attn_args *args, int B, int Lq, int
 /*
  * dsa_forward with the latent rows in the 4-bit cache (the indexer's keys stay e4m3).
  *   sel_scores: as dsa_forward_timed (may be NULL); workspace: as dsa_forward (DSA_OP_FORWARD
- *   or DSA_OP_FORWARD_LOWMEM); short sequences as there.
+ *   or DSA_OP_FORWARD_LOWMEM), or DSA_OP_FORWARD_KV4 with the room that dsa_sparse_attn_kv4
+ *   describes; short sequences as there.
  */
 dsa_status dsa_forward_kv4(const dsa_indexer_args *iargs, const dsa_kv4_attn_args *kargs, int k, int32_t *indices,
                            float *sel_scores, void *out, float *lse, void *workspace, size_t workspace_bytes,

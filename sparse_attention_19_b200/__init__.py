@@ -25,12 +25,14 @@ __all__ = [
     "window_attn",
     "workspace_size", "workspace_size_args", "status_string", "device_status", "selftest_wait_timeout", "version",
     "OP_TOPK", "OP_SPARSE_ATTN", "OP_FORWARD", "OP_INDEXER_TOPK", "OP_FORWARD_LOWMEM", "OP_WINDOW_ATTN",
+    "OP_SPARSE_ATTN_KV4", "OP_FORWARD_KV4",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 lib_path = os.path.join(_HERE, "libdsa.so")
 
 OP_TOPK, OP_SPARSE_ATTN, OP_FORWARD, OP_INDEXER_TOPK, OP_FORWARD_LOWMEM, OP_WINDOW_ATTN = 0, 1, 2, 3, 4, 5
+OP_SPARSE_ATTN_KV4, OP_FORWARD_KV4 = 6, 7
 _STATUS = {0: "DSA_OK", 1: "DSA_ERR_INVALID_ARG", 2: "DSA_ERR_UNSUPPORTED", 3: "DSA_ERR_WORKSPACE",
            4: "DSA_ERR_CUDA", 5: "DSA_ERR_TIMEOUT"}
 
@@ -622,7 +624,9 @@ def _attn_outputs(q, d_v, out, lse, want_lse):
 def sparse_attn_kv4(q, codes, scales, tail, indices, scale, out=None, lse=None, want_lse=True, workspace=None,
                     stream=None):
     """sparse_attn over the rows of a 4-bit cache (kv4_cache): bf16 [B, Lq, H, d_v] and fp32
-    lse [B, Lq, H].  Rows that ``indices`` does not name may hold anything."""
+    lse [B, Lq, H].  Rows that ``indices`` does not name may hold anything.  Without a
+    ``workspace`` of the caller's, a prefill chunk takes one with room for the unpacked rows
+    (OP_SPARSE_ATTN_KV4); OP_SPARSE_ATTN bytes do, and are slower there."""
     c, a = _kv4_attn_args(q, codes, scales, tail, scale)
     dev, Lq, k = q.device, q.shape[1], indices.shape[-1]
     _need_at(indices, torch.int32, (c.B, Lq, k), "indices", dev)
@@ -630,7 +634,7 @@ def sparse_attn_kv4(q, codes, scales, tail, indices, scale, out=None, lse=None, 
 
     def call(st):
         o, l = _attn_outputs(q, c.d_v, out, lse, want_lse)
-        ws, nbytes = _workspace(OP_SPARSE_ATTN, c.B, Lq, max(c.Lk, Lq), k, a.H, c.d_v, dev, workspace)
+        ws, nbytes = _workspace(OP_SPARSE_ATTN_KV4, c.B, Lq, c.Lk, k, a.H, c.d_v, dev, workspace)
         _check(lib().dsa_sparse_attn_kv4(ctypes.byref(a), c.B, Lq, c.Lk, indices.data_ptr(), k, o.data_ptr(), _ptr(l),
                                          _ptr(ws), nbytes, st), "dsa_sparse_attn_kv4")
         return o, l
@@ -640,7 +644,8 @@ def sparse_attn_kv4(q, codes, scales, tail, indices, scale, out=None, lse=None, 
 
 def forward_kv4(q_I, q_scale, w, k_I, k_scale, q, codes, scales, tail, k, scale, q_offset=0, indices=None, out=None,
                 lse=None, want_lse=True, workspace=None, stream=None, sel_scores=None, low_memory=False):
-    """forward with the latent rows in a 4-bit cache.  Returns (indices, out, lse)."""
+    """forward with the latent rows in a 4-bit cache.  Returns (indices, out, lse).  With
+    ``low_memory`` neither scores nor unpacked rows are held (sparse_attn_kv4)."""
     k, q_offset = _int32(k, "k"), _int32(q_offset, "q_offset")
     c, a = _kv4_attn_args(q, codes, scales, tail, scale)
     dev = q.device
@@ -658,8 +663,8 @@ def forward_kv4(q_I, q_scale, w, k_I, k_scale, q, codes, scales, tail, k, scale,
         i = torch.empty(ia.B, ia.Lq, k, dtype=torch.int32, device=dev) if indices is None else indices
         _need_at(i, torch.int32, (ia.B, ia.Lq, k), "indices", dev)
         o, l = _attn_outputs(q, c.d_v, out, lse, want_lse)
-        ws, nbytes = _workspace(OP_FORWARD_LOWMEM if low_memory else OP_FORWARD, ia.B, ia.Lq, ia.Lk, k, a.H, c.d_v,
-                                dev, workspace, ia=ia)
+        ws, nbytes = _workspace(OP_FORWARD_LOWMEM if low_memory else OP_FORWARD_KV4, ia.B, ia.Lq, ia.Lk, k, a.H,
+                                c.d_v, dev, workspace, ia=ia)
         _check(lib().dsa_forward_kv4(ctypes.byref(ia), ctypes.byref(a), k, _ptr(i), _ptr(sel_scores), _ptr(o),
                                      _ptr(l), _ptr(ws), nbytes, st), "dsa_forward_kv4")
         return i, o, l

@@ -21,6 +21,7 @@ namespace dsa {
 namespace {
 
 constexpr int kMaxK = 2048;
+constexpr int kRopeDim = 64;         // d_qk - d_v of every supported latent row
 constexpr int kAttnTile = 128;
 constexpr long long kTopkCacheMax = 8192;
 
@@ -341,11 +342,12 @@ dsa_status run_topk(const float* scores, int B, int Lq, int Lk, int q_offset, in
 // tiles, with the index lists 0..t written to dense_idx_out by the same kernel.
 dsa_status run_attn(const dsa_attn_args* a, int B, int Lq, int Lk, int q_offset, bool compact,
                     const int32_t* idx, int k, void* out, float* lse, void* ws, size_t ws_bytes,
-                    cudaStream_t st, int32_t* dense_idx_out = nullptr) {
+                    cudaStream_t st, int32_t* dense_idx_out = nullptr, bool zero_row_behind = false) {
   AttnParams p{};
   p.B = B; p.Lq = Lq; p.Lk = Lk; p.H = a->H; p.k = k;
   p.dense = dense_idx_out ? 1 : 0;
   p.idx_out = dense_idx_out;
+  p.zero_row = zero_row_behind ? B * Lk : 0;
   if (p.dense) compact = true;
   p.n_tiles = (k + kAttnTile - 1) / kAttnTile;
   const int rows = B * Lq;
@@ -369,8 +371,8 @@ dsa_status run_attn(const dsa_attn_args* a, int B, int Lq, int Lk, int q_offset,
   if (!make_tmap(&tq, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, a->q, (uint64_t)rows * a->H, a->d_qk, 64, 64,
                  CU_TENSOR_MAP_SWIZZLE_128B))
     return DSA_ERR_CUDA;
-  if (!make_tmap(&tkv, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, a->kv, (uint64_t)B * Lk, a->d_qk, 64, 1,
-                 CU_TENSOR_MAP_SWIZZLE_128B))
+  if (!make_tmap(&tkv, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, a->kv, (uint64_t)B * Lk + (zero_row_behind ? 1 : 0), a->d_qk, 64,
+                 1, CU_TENSOR_MAP_SWIZZLE_128B))
     return DSA_ERR_CUDA;
   CUtensorMap tkv_tile = tkv;                               // 64 contiguous rows per box (dense mode)
   if (p.dense && !make_tmap(&tkv_tile, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, a->kv, (uint64_t)B * Lk, a->d_qk, 64,
@@ -418,10 +420,43 @@ dsa_status launch_attn_mode(AttnParams p, const void* q, const void* kv, int d_q
   return DSA_OK;
 }
 
+// Whether the attention over the 4-bit cache unpacks the cache into the workspace and attends
+// over bf16 rows: when the lists name each row often enough.  Converting inside the attention
+// costs 0.06 ns more per named row than gathering bf16 rows (16 heads: 0.07); unpacking costs 0.4 ns
+// per cache row and a launch.  Both ways in us, 128 heads, k = 2048 (uses of a row): 1024 rows over 32768
+// (64) 746 in the kernel, 621 unpacked; 128 over 4096 (64) 116, 102; 256 over 32768 (16) 293, 269;
+// 512 over 131072 (8) 452, 428; 256 over 131072 (4) 298, 297; the launch shows below 131072 named rows:
+// 64 over 4096 62, 60; 40 over 4096 68, 70; 300 over 300 with k = 256 57, 61.
+bool kv4_unpacks(int B, int Lq, int Lk, int k) {
+  const long long slots = (long long)B * Lq * (k < Lk ? k : Lk), rows = (long long)B * Lk;
+  return slots >= 8 * rows + 131072 && rows + 1 < (1LL << 31);
+}
+// Bytes behind the attention's own workspace that this takes: the rows and one of zeros.
+size_t kv4_unpack_bytes(int B, int Lq, int Lk, int k, int d_qk) {
+  return kv4_unpacks(B, Lq, Lk, k) ? 256 + ((size_t)B * Lk + 1) * d_qk * 2 : 0;
+}
+
 // Attention over the 4-bit cache; `dense_idx_out` as in run_attn.
 dsa_status run_attn_kv4(const dsa_kv4_attn_args* a, int B, int Lq, int Lk, int q_offset, bool compact,
                         const int32_t* idx, int k, void* out, float* lse, void* ws, size_t ws_bytes, cudaStream_t st,
                         int32_t* dense_idx_out = nullptr) {
+  // Not for dense rows: their boxes take rows behind the query, which may hold a NaN.
+  const size_t unpack = dense_idx_out ? 0 : kv4_unpack_bytes(B, Lq, Lk, k, a->d_qk);
+  const size_t attn_need = attn_ws_bytes(B, Lq, k, a->H, a->d_v);
+  if (unpack && ws && aligned16(ws) && ws_bytes >= attn_need + unpack) {
+    char* rows = static_cast<char*>(ws) + round_up(attn_need, 256);
+    Kv4Params r{};
+    r.div_l = fast_div((uint32_t)Lk);
+    r.B = B; r.L = Lk; r.Lk = Lk; r.d_qk = a->d_qk; r.d_v = a->d_v;
+    r.zero_rows = 1;
+    r.out = reinterpret_cast<__nv_bfloat16*>(rows);
+    r.codes = const_cast<uint8_t*>(reinterpret_cast<const uint8_t*>(a->codes));
+    r.scales = const_cast<__nv_bfloat16*>(reinterpret_cast<const __nv_bfloat16*>(a->scales));
+    r.tail = const_cast<__nv_bfloat16*>(reinterpret_cast<const __nv_bfloat16*>(a->tail));
+    if (launch_kv4_read(r, st) != cudaSuccess) return DSA_ERR_CUDA;
+    const dsa_attn_args b{a->H, a->d_qk, a->d_v, a->scale, a->q, rows};
+    return run_attn(&b, B, Lq, Lk, q_offset, compact, idx, k, out, lse, ws, attn_need, st, nullptr, true);
+  }
   AttnParams p{};
   p.B = B; p.Lq = Lq; p.Lk = Lk; p.H = a->H; p.k = k;
   p.dense = dense_idx_out ? 1 : 0;
@@ -740,6 +775,13 @@ size_t dsa_workspace_size_args(dsa_op op, const dsa_indexer_args* iargs, int k, 
       const size_t sel = indexer_topk_ws_bytes(iargs, k);
       return sel ? round_up(sel, 256) + attn_ws_bytes(iargs->B, iargs->Lq, k, H, d_v) : 0;
     }
+    case DSA_OP_FORWARD_KV4:
+    case DSA_OP_SPARSE_ATTN_KV4: {
+      if (H <= 0 || d_v <= 0) return 0;
+      return (op == DSA_OP_FORWARD_KV4 ? scores_ws_bytes(iargs) : 0) +
+             attn_ws_bytes(iargs->B, iargs->Lq, k, H, d_v) +
+             kv4_unpack_bytes(iargs->B, iargs->Lq, iargs->Lk, k, d_v + kRopeDim);
+    }
     case DSA_OP_WINDOW_ATTN:
       break;
   }
@@ -747,11 +789,15 @@ size_t dsa_workspace_size_args(dsa_op op, const dsa_indexer_args* iargs, int k, 
 }
 
 size_t dsa_workspace_size(dsa_op op, int B, int Lq, int Lk, int k, int H, int d_v) {
-  if (B <= 0 || Lq <= 0 || Lk <= 0 || Lq > Lk || k < 1 || H <= 0 || d_v <= 0) return 0;
+  if (B <= 0 || Lq <= 0 || Lk <= 0 || k < 1 || H <= 0 || d_v <= 0) return 0;
+  if (op == DSA_OP_SPARSE_ATTN_KV4)
+    return k > kMaxK ? 0 : attn_ws_bytes(B, Lq, k, H, d_v) + kv4_unpack_bytes(B, Lq, Lk, k, d_v + kRopeDim);
+  if (Lq > Lk) return 0;
   if (op == DSA_OP_WINDOW_ATTN) return attn_ws_bytes(B, Lq, k < Lk ? k : Lk, H, d_v);
   if (k > kMaxK) return 0;
   switch (op) {
     case DSA_OP_WINDOW_ATTN:
+    case DSA_OP_SPARSE_ATTN_KV4:
       break;
     case DSA_OP_TOPK:
       return 0;
@@ -759,6 +805,7 @@ size_t dsa_workspace_size(dsa_op op, int B, int Lq, int Lk, int k, int H, int d_
       return attn_ws_bytes(B, Lq, k, H, d_v);
     case DSA_OP_INDEXER_TOPK:
     case DSA_OP_FORWARD:
+    case DSA_OP_FORWARD_KV4:
     case DSA_OP_FORWARD_LOWMEM: {
       // The documented convention: H_I = 64, d_I = 128, q_offset = Lk - Lq.
       alignas(16) static const uint8_t dummy[16] = {};

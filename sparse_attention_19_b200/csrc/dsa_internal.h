@@ -110,6 +110,9 @@ struct AttnParams {
   // keys (t - window, t] and [0, sinks); no index lists
   int window, sinks;
   const int32_t* start;   // [B] or null
+  // ---- lists over rows with one row of zeros behind them: the row that masked slots gather
+  // (0: they gather the sequence's first row)
+  int zero_row;
   // ---- 4-bit cache (codes set): indices (or dense) pick its rows
   const uint8_t* codes;   // [B, Lk, d_v / 2]
   const __nv_bfloat16* scales;   // [B, Lk, d_v / 32]
@@ -196,6 +199,7 @@ cudaError_t launch_norm_rope_bwd(NormRopeParams p, int sms, cudaStream_t stream)
 struct Kv4Params {
   FastDiv div_l;          // by L
   int B, L, Lk, d_qk, d_v;
+  int zero_rows;          // read: rows of zeros written behind the last
   int offset;             // cache row of row 0 when start is null
   const int32_t* start;   // [B] or null
   const __nv_bfloat16* in;    // write: [B, L, d_qk]

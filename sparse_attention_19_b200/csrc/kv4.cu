@@ -119,6 +119,7 @@ __global__ void __launch_bounds__(kThreads) kv4_read_kernel(const Kv4Params p) {
   griddep_launch_dependents();
   griddep_wait();
   const int tail8 = (p.d_qk - DV) / 8, c = lane / 4, part = lane % 4, n = p.B * p.L;
+  const int n_out = n + p.zero_rows;
   uint2 code[kReadRows];
   uint32_t step[kReadRows];
   uint4 t[kReadRows];
@@ -138,7 +139,7 @@ __global__ void __launch_bounds__(kThreads) kv4_read_kernel(const Kv4Params p) {
 #pragma unroll
   for (int i = 0; i < kReadRows; ++i) {
     const int row = row0 + i * S::kRows;
-    if (row >= n) return;
+    if (row >= n_out) return;
     const Kv4Step s = kv4_step(step[i]);
     uint4* dst = reinterpret_cast<uint4*>(p.out + (size_t)row * p.d_qk);
     dst[2 * lane] = unpack_codes(code[i].x, s);
@@ -148,7 +149,7 @@ __global__ void __launch_bounds__(kThreads) kv4_read_kernel(const Kv4Params p) {
 }
 
 unsigned blocks(const Kv4Params& p, int rows_per_block) {
-  return (unsigned)(((long long)p.B * p.L + rows_per_block - 1) / rows_per_block);
+  return (unsigned)(((long long)p.B * p.L + p.zero_rows + rows_per_block - 1) / rows_per_block);
 }
 
 }  // namespace

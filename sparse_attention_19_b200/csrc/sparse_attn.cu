@@ -54,7 +54,9 @@
 //   * rows of the 4-bit cache (kPacked): 16 warps convert codes to bf16 planes in shared
 //     memory, in the layouts TMA writes for bf16 rows, once as key chunks and once as
 //     value stages.  Everything behind the operands is shared, so the result equals the bf16
-//     kernel's over the values that the cache holds bit for bit.
+//     kernel's over the values that the cache holds bit for bit.  Meant for rows used a few times
+//     (decode); a chunk of queries that use each row many times has the cache unpacked first and runs
+//     kSelected, with masked slots gathering a row of zeros (the host's rule has the figures).
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -573,6 +575,7 @@ sparse_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
       return;
     }
     const int32_t* src = p.indices + (size_t)V.row * p.k;
+    const int first = V.b * p.Lk, masked = p.zero_row ? p.zero_row : first;
     for (int w0 = pw; w0 < nwords; w0 += kStageWarps * kStageBatch) {
       int sidx[kStageBatch];
 #pragma unroll
@@ -585,7 +588,7 @@ sparse_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
         const int w = w0 + e * kStageWarps;
         if (w >= nwords) break;                       // warp-uniform
         const bool valid = (sidx[e] >= 0) && (sidx[e] < p.Lk);
-        if (MODE != kPacked) dst[w * 32 + (int)lane] = V.b * p.Lk + (valid ? sidx[e] : 0);   // validity: the ballot below
+        if (MODE != kPacked) dst[w * 32 + (int)lane] = valid ? first + sidx[e] : masked;   // validity: the ballot below
         const uint32_t bal = __ballot_sync(0xffffffffu, valid);
         if (lane == 0) vmask[w] = bal;
       }

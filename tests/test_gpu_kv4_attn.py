@@ -124,6 +124,97 @@ def test_many_units_per_cluster_and_long_rows():
     assert torch.equal(out, o2) and torch.equal(lse, l2)
 
 
+def _both_ways(q, cache, idx):
+    """Over the unpacked rows (the workspace that the binding takes) and in the kernel (the least one)."""
+    B, Lq, H, D = q.shape
+    d_v = 2 * cache[0].shape[-1]
+    Lk, k = cache[0].shape[1], idx.shape[-1]
+    assert dsa.workspace_size(dsa.OP_SPARSE_ATTN_KV4, B, Lq, Lk, k, H, d_v) > B * Lk * D * 2, "the rule does not unpack"
+    least = max(dsa.workspace_size(dsa.OP_SPARSE_ATTN, B, Lq, max(Lk, Lq), k, H, d_v), 16)
+    return (dsa.sparse_attn_kv4(q, *cache, idx, SCALE),
+            dsa.sparse_attn_kv4(q, *cache, idx, SCALE, workspace=torch.empty(least, device=DEV, dtype=torch.uint8)))
+
+
+@pytest.mark.parametrize("shape", ["mla", "tiny"])
+@pytest.mark.parametrize("kind", ["prefix", "holes"])
+@pytest.mark.parametrize("B,Lq,Lk,k", [(1, 600, 3000, 1000), (3, 200, 1111, 513), (2, 3000, 40, 48), (1, 70, 65, 2048 - 31),
+                                       (1, 7, 1, 1)])
+def test_unpacked_rows_give_the_same_bits(shape, kind, B, Lq, Lk, k):
+    if Lq * Lk * B < 140000:                               # enough slots for the rule
+        Lq = 140000 // (B * Lk) + 1
+    if shape == "mla" and Lq > 10000:
+        pytest.skip("20 GB of queries; the narrow shape covers it")
+    q, kv, d_v, g = _inputs(shape, B, Lq, Lk, 17)
+    cache = _cache(kv, d_v)
+    idx = _indices(g, B, Lq, Lk, k, kind)
+    idx[0, 1::13] = -1
+    (o, l), (o2, l2) = _both_ways(q, cache, idx)
+    assert torch.equal(o, o2) and torch.equal(l, l2)
+    n = B * Lq
+    _check(q, cache, idx, d_v, o, l, [0, 1, n // 2, n - 1])
+
+
+@pytest.mark.parametrize("shape", ["mla", "tiny"])
+def test_unpacked_rows_that_are_not_selected_may_hold_anything(shape):
+    q, kv, d_v, g = _inputs(shape, 2, 400, 900, 3)
+    cache = _cache(kv, d_v)
+    idx = _indices(g, 2, 400, 900, 300, "holes")
+    idx = torch.where(idx % 3 == 1, idx, -1)               # row 0 among those never named
+    want = dsa.sparse_attn_kv4(q, *cache, idx, SCALE)
+    bad = torch.arange(900, device=DEV) % 3 != 1
+    cache[0][:, bad] = 0
+    cache[1][:, bad] = float("nan")
+    cache[2][:, bad] = float("inf")
+    for o, l in _both_ways(q, cache, idx):
+        assert torch.equal(o, want[0]) and torch.equal(l, want[1])
+    # a NaN reaches the queries that select its row and no other
+    cache[1][0, 0] = float("nan")
+    cache[2][0, 0] = 0
+    idx[0, 5, 7] = 0
+    for o, _ in _both_ways(q, cache, idx):
+        assert o[0, 5].isnan().any()
+        hit = torch.zeros(2, 400, dtype=torch.bool, device=DEV)
+        hit[0, 5] = True
+        assert torch.equal(o[~hit], want[0][~hit])
+
+
+def test_unpacked_rows_two_calls_at_once_and_from_a_graph():
+    q, kv, d_v, g = _inputs("mla", 1, 300, 1500, 9)
+    cache, other = _cache(kv, d_v), _cache(kv.flip(1), d_v)
+    idx = _indices(g, 1, 300, 1500, 600, "prefix")
+    want, want2 = (_both_ways(q, c, idx)[1] for c in (cache, other))
+    s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+    for s in (s1, s2):
+        s.wait_stream(torch.cuda.current_stream())
+    got = [dsa.sparse_attn_kv4(q, *(other if i % 2 else cache), idx, SCALE, stream=s2 if i % 2 else s1) for i in range(6)]
+    s1.synchronize()
+    s2.synchronize()
+    for i, (o, l) in enumerate(got):
+        wo, wl = want2 if i % 2 else want
+        assert torch.equal(o, wo) and torch.equal(l, wl)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        o, l = dsa.sparse_attn_kv4(q, *cache, idx, SCALE)
+    for a, b in zip(cache, other):
+        a.copy_(b)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(o, want2[0]) and torch.equal(l, want2[1])
+
+
+def test_forward_over_unpacked_rows():
+    wl = WORKLOADS["prefill_8k"].with_(B=1, Lq=700, Lk=4200, q_offset=3500)
+    inp = make_inputs(wl, DEV, 1)
+    cache = _cache(inp["kv"], wl.Dv)
+    side = [inp[x] for x in ("q_I", "q_scale", "w", "k_I", "k_scale")]
+    assert dsa.workspace_size(dsa.OP_FORWARD_KV4, 1, 700, 4200, wl.k, 128, 512) > \
+        dsa.workspace_size(dsa.OP_FORWARD, 1, 700, 4200, wl.k, 128, 512) + 4200 * 576 * 2
+    got = dsa.forward_kv4(*side, inp["q"], *cache, wl.k, wl.scale, wl.q_offset)
+    low = dsa.forward_kv4(*side, inp["q"], *cache, wl.k, wl.scale, wl.q_offset, low_memory=True)
+    assert all(torch.equal(a, b) for a, b in zip(got, low))
+    _check(inp["q"], cache, got[0], wl.Dv, got[1], got[2], [0, 350, 699])
+
+
 def test_rows_behind_four_gigabytes():
     q, kv, d_v, g = _inputs("mla", 2, 1, 64, 6)
     Lk = 9_000_000                                         # 2 x 2.3 GB of codes

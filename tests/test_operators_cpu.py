@@ -135,6 +135,18 @@ def test_kv4_attention_refuses_the_rest(L):
     assert L.dsa_forward_kv4(ctypes.byref(ia), ctypes.byref(a), 8, P, None, P, None, P, 255, None) == WORKSPACE
 
 
+def test_kv4_workspace_holds_unpacked_rows_where_lists_repeat_them():
+    size = dsa.workspace_size
+    for B, Lq, Lk, k in [(64, 1, 32768, 2048), (1, 100, 131072, 2048), (1, 30, 100, 100)]:      # few uses of a row
+        assert size(dsa.OP_SPARSE_ATTN_KV4, B, Lq, Lk, k, 128, 512) == size(dsa.OP_SPARSE_ATTN, B, Lq, Lk, k, 128, 512)
+    for B, Lq, Lk, k in [(1, 1024, 32768, 2048), (4, 800, 1000, 2048), (1, 4000, 100, 300)]:
+        least = size(dsa.OP_SPARSE_ATTN, B, Lq, max(Lq, Lk), k, 128, 512)
+        assert size(dsa.OP_SPARSE_ATTN_KV4, B, Lq, Lk, k, 128, 512) >= least + (B * Lk + 1) * 576 * 2
+    for op in (dsa.OP_SPARSE_ATTN_KV4, dsa.OP_FORWARD_KV4):
+        assert size(op, 0, 1, 8, 8, 128, 512) == size(op, 1, 1, 8, 2049, 128, 512) == size(op, 1, 1, 8, 0, 128, 512) == 0
+    assert size(dsa.OP_FORWARD_KV4, 1, 1, 4096, 2048, 128, 512) == size(dsa.OP_FORWARD, 1, 1, 4096, 2048, 128, 512) > 0
+
+
 def test_window_attention_refuses(L):
     good = dsa.AttnArgs(128, 576, 512, 0.07, 16, 16)
     f = L.dsa_window_attn
