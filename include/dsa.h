@@ -126,7 +126,8 @@ dsa_status dsa_indexer_topk(const dsa_indexer_args *args, int k, int32_t *indice
  *   out:     bf16 [B, Lq, H, d_v];  out[b,i,h,:] = sum_s p_s kv[b,s,:d_v],
  *            p = softmax over the selected s of scale * q[b,i,h,:] . kv[b,s,:].
  *   lse:     fp32 [B, Lq, H] or NULL; natural-log log-sum-exp of the logits
- *            (-INFINITY and out = 0 for a row with no valid entry).
+ *            (-INFINITY and out = 0 for a row with no valid entry).  A NaN in a row
+ *            that a query attends to, or a logit of +INFINITY, makes its out and lse NaN.
  * Rows with B*Lq small are split over the k entries across CTAs and merged
  * (split-k); the workspace holds the partial results.
  */

@@ -1049,8 +1049,10 @@ sparse_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
       const float total = lsum + S.red_sum[l ^ 64u];
       ok = warps_rendezvous(&S.xbar[warp & 1u], xph, abort_flag);   // red_sum may be rewritten next unit
       if (!ok) break;
-      const float inv = total > 0.f ? 1.f / total : 0.f;
-      const float lse_v = total > 0.f ? (m + log2f(total)) * kLn2 : -INFINITY;
+      // A NaN logit (or one of +inf, minus the maximum) is in the sum, though a maximum passes
+      // it over: out and lse are NaN then, and the merge of a split row carries it on.
+      const float inv = total > 0.f ? 1.f / total : total;
+      const float lse_v = total > 0.f ? (m + log2f(total)) * kLn2 : total == 0.f ? -INFINITY : total;
       const bool write = head < p.H;
       for (int hi = 0; hi < VS::kNpv; ++hi) {
         for (int c0 = 0; c0 < VS::kN / 2; c0 += 32) {
@@ -1103,6 +1105,7 @@ sparse_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
 }
 
 // Merge split-k partials: lse = log sum_i exp(lse_i); out = sum_i exp(lse_i - lse) o_i.
+// A split whose lse is NaN makes the row's out and lse NaN.
 template <int DV>
 __global__ void __launch_bounds__(128) attn_combine_kernel(const AttnParams p) {
   griddep_launch_dependents();
@@ -1114,13 +1117,17 @@ __global__ void __launch_bounds__(128) attn_combine_kernel(const AttnParams p) {
   if (gw >= n) return;
   const int row = gw / p.H, head = gw % p.H;
   float mx = -INFINITY;
-  for (int sp = 0; sp < p.splits; ++sp)
-    mx = fmaxf(mx, p.part_lse[((size_t)row * p.splits + sp) * p.H + head]);
+  bool any = false;                                    // a split saw something
+  for (int sp = 0; sp < p.splits; ++sp) {
+    const float l = p.part_lse[((size_t)row * p.splits + sp) * p.H + head];
+    mx = fmaxf(mx, l);
+    any = any || l != -INFINITY;
+  }
   float wsum = 0.f;
   float acc[DV / 32];
 #pragma unroll
   for (int e = 0; e < DV / 32; ++e) acc[e] = 0.f;
-  if (mx > -INFINITY) {
+  if (any) {
     for (int sp = 0; sp < p.splits; ++sp) {
       const size_t prow = ((size_t)row * p.splits + sp) * p.H + head;
       const float wgt = expf(p.part_lse[prow] - mx);
@@ -1130,11 +1137,11 @@ __global__ void __launch_bounds__(128) attn_combine_kernel(const AttnParams p) {
       for (int e = 0; e < DV / 32; ++e) acc[e] = fmaf(wgt, src[e * 32 + lane], acc[e]);
     }
   }
-  const float inv = wsum > 0.f ? 1.f / wsum : 0.f;
+  const float inv = wsum > 0.f ? 1.f / wsum : wsum;
   __nv_bfloat16* dst = p.out + ((size_t)row * p.H + head) * DV;
 #pragma unroll
   for (int e = 0; e < DV / 32; ++e) dst[e * 32 + lane] = __float2bfloat16_rn(acc[e] * inv);
-  if (lane == 0 && p.lse) p.lse[(size_t)row * p.H + head] = (wsum > 0.f) ? mx + logf(wsum) : -INFINITY;
+  if (lane == 0 && p.lse) p.lse[(size_t)row * p.H + head] = wsum > 0.f ? mx + logf(wsum) : wsum == 0.f ? -INFINITY : wsum;
 }
 
 template <int NC, int DV, int MODE>
