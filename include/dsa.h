@@ -288,8 +288,9 @@ typedef struct {
  * scale == NULL: out is bf16 [B, L, H, D], contiguous, y rounded once.
  * Otherwise out is e4m3 [B, L, H, D] and scale fp32 [B, L], as the indexer takes them
  *   (dsa_indexer_args q_I/q_scale, or k_I/k_scale with H = 1): scale = max(amax of |y|
- *   over the token's heads, 1e-30) / 448, code = rne(y / scale).  A token with a NaN has a
- *   NaN scale.
+ *   over the token's heads, 1e-30) / 448, code = rne(y / scale), both quotients in fp32.  A
+ *   token with a NaN has a NaN scale; one with an infinity has an infinite scale, zeros for its
+ *   finite values and NaN codes for the infinite ones.
  * out must not overlap x.
  */
 dsa_status dsa_norm_rope(const dsa_norm_rope_args *args, void *out, float *scale, void *stream);

@@ -312,15 +312,33 @@ struct Walk {
   }
 };
 
-__device__ __forceinline__ uint2 to_e4m3(const Vec8& y, float2 inv) {
-  uint32_t code[4];
-#pragma unroll
-  for (int e = 0; e < 4; ++e) code[e] = __nv_cvt_float2_to_fp8x2(fmul2(y.v[e], inv), __NV_SATFINITE, __NV_E4M3);
-  return make_uint2(code[0] | (code[1] << 16), code[2] | (code[3] << 16));
+// amax / 448 and y / scale, each as a product with a reciprocal of two floats whose sum is off
+// by less than 2^-44 of itself.  The product's one rounding then gives the rounded quotient
+// unless that lies so close to the middle of two floats, which no fp32 value over 448 and no bf16
+// value over an fp32 one does: a quotient on the border of two codes stays there.  (The
+// bare product with one float crosses it for 1 in 1000 pairs of bf16 significands.)
+// Infinities take no second float (inf - inf, 0 * inf): with an infinite scale, finite
+// values become 0 and the infinite ones NaN.
+__device__ __forceinline__ float scale_of(float amax) {
+  constexpr float hi = 1.f / 448.f, lo = (float)(1.0 / 448.0 - (double)hi);
+  return isinf(amax) ? amax : fmaf(amax, hi, amax * lo);
+}
+struct Reciprocal {
+  float2 hi, lo;
+};
+__device__ __forceinline__ Reciprocal reciprocal(float scale) {
+  float hi;
+  asm("rcp.approx.f32 %0, %1;" : "=f"(hi) : "f"(scale));
+  return {both(hi), both(isinf(scale) ? 0.f : fmaf(-scale, hi, 1.f) * hi)};
 }
 
-// 1/scale; y / scale is computed as y * (1 / scale), a few fp32 steps from the quotient at most.
-__device__ __forceinline__ float inv_scale(float amax) { return 1.f / (amax * (1.f / 448.f)); }
+__device__ __forceinline__ uint2 to_e4m3(const Vec8& y, const Reciprocal& r) {
+  uint32_t code[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e)
+    code[e] = __nv_cvt_float2_to_fp8x2(ffma2(y.v[e], r.hi, fmul2(y.v[e], r.lo)), __NV_SATFINITE, __NV_E4M3);
+  return make_uint2(code[0] | (code[1] << 16), code[2] | (code[3] << 16));
+}
 
 // bf16 output.  Persistent blocks; while a step is computed the next one's rows are in
 // flight, and one barrier per span completes its angles.  Bound by HBM: 0.86-0.90 of the copy
@@ -455,13 +473,13 @@ __global__ void __launch_bounds__(kThreads, resident_e4m3(2 * NP + NM, LAYER)) n
         atomicMax(reinterpret_cast<int*>(&amax[r.tok - first]), __float_as_int(m));
       for (int t = threadIdx.x; t < p.tokens_per_step; t += kThreads) amax_next[t] = kAmaxFloor;
       __syncthreads();
-      if (threadIdx.x < q.count(p)) p.scale[first + threadIdx.x] = amax[threadIdx.x] / 448.f;
+      if (threadIdx.x < q.count(p)) p.scale[first + threadIdx.x] = scale_of(amax[threadIdx.x]);
       if (!r.here) continue;
-      const float2 inv = both(inv_scale(amax[r.tok - first]));
+      const Reciprocal by = reciprocal(scale_of(amax[r.tok - first]));
       uint2* dst = reinterpret_cast<uint2*>(p.codes) + r.offset(p);
 #pragma unroll
       for (int n = 0; n < N; ++n)
-        if (slots.has(n)) dst[slots.vec(n)] = to_e4m3(y[n], inv);
+        if (slots.has(n)) dst[slots.vec(n)] = to_e4m3(y[n], by);
     }
   }
 }
@@ -509,11 +527,11 @@ __global__ void __launch_bounds__(kThreads) norm_rope_wide_kernel(const NormRope
 #pragma unroll
           for (int e = 0; e < 4; ++e) m = max_abs(m, y[n].v[e].x, y[n].v[e].y);
       } else {
-        const float2 inv = both(inv_scale(amax));
+        const Reciprocal by = reciprocal(scale_of(amax));
         uint2* dst = reinterpret_cast<uint2*>(p.codes) + ((size_t)tok * p.H + h) * (p.D / 8);
 #pragma unroll
         for (int n = 0; n < N; ++n)
-          if (slots.has(n)) dst[slots.vec(n)] = to_e4m3(y[n], inv);
+          if (slots.has(n)) dst[slots.vec(n)] = to_e4m3(y[n], by);
       }
     }
     if (pass == 0) {
@@ -521,7 +539,7 @@ __global__ void __launch_bounds__(kThreads) norm_rope_wide_kernel(const NormRope
       for (int o = 16; o > 0; o >>= 1) m = max_abs(m, __shfl_xor_sync(0xffffffffu, m, o), 0.f);
       if (threadIdx.x % 32 == 0) atomicMax(reinterpret_cast<int*>(&amax), __float_as_int(m));
       __syncthreads();
-      if (threadIdx.x == 0) p.scale[tok] = amax / 448.f;
+      if (threadIdx.x == 0) p.scale[tok] = scale_of(amax);
     }
   }
 }
