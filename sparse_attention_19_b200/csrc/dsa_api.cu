@@ -790,19 +790,21 @@ size_t dsa_workspace_size_args(dsa_op op, const dsa_indexer_args* iargs, int k, 
 
 size_t dsa_workspace_size(dsa_op op, int B, int Lq, int Lk, int k, int H, int d_v) {
   if (B <= 0 || Lq <= 0 || Lk <= 0 || k < 1 || H <= 0 || d_v <= 0) return 0;
-  if (op == DSA_OP_SPARSE_ATTN_KV4)
-    return k > kMaxK ? 0 : attn_ws_bytes(B, Lq, k, H, d_v) + kv4_unpack_bytes(B, Lq, Lk, k, d_v + kRopeDim);
+  // The attentions over index lists take more queries than cache rows too.
+  if (op == DSA_OP_SPARSE_ATTN || op == DSA_OP_SPARSE_ATTN_KV4)
+    return k > kMaxK ? 0
+                     : attn_ws_bytes(B, Lq, k, H, d_v) +
+                           (op == DSA_OP_SPARSE_ATTN_KV4 ? kv4_unpack_bytes(B, Lq, Lk, k, d_v + kRopeDim) : 0);
   if (Lq > Lk) return 0;
   if (op == DSA_OP_WINDOW_ATTN) return attn_ws_bytes(B, Lq, k < Lk ? k : Lk, H, d_v);
   if (k > kMaxK) return 0;
   switch (op) {
     case DSA_OP_WINDOW_ATTN:
+    case DSA_OP_SPARSE_ATTN:
     case DSA_OP_SPARSE_ATTN_KV4:
       break;
     case DSA_OP_TOPK:
       return 0;
-    case DSA_OP_SPARSE_ATTN:
-      return attn_ws_bytes(B, Lq, k, H, d_v);
     case DSA_OP_INDEXER_TOPK:
     case DSA_OP_FORWARD:
     case DSA_OP_FORWARD_KV4:

@@ -215,6 +215,20 @@ def test_forward_over_unpacked_rows():
     _check(inp["q"], cache, got[0], wl.Dv, got[1], got[2], [0, 350, 699])
 
 
+@pytest.mark.parametrize("shape", ["mla", "tiny"])
+@pytest.mark.parametrize("B,Lq,Lk,k", [(1, 4, 3, 2048), (2, 9, 1, 700)])
+def test_more_queries_than_cache_rows(shape, B, Lq, Lk, k):
+    q, kv, d_v, g = _inputs(shape, B, Lq, Lk, 21)
+    cache = _cache(kv, d_v)
+    idx = _indices(g, B, Lq, Lk, k, "holes")
+    need = dsa.workspace_size(dsa.OP_SPARSE_ATTN, B, Lq, Lk, k, q.shape[2], d_v)
+    assert need > 0
+    out, lse = dsa.sparse_attn_kv4(q, *cache, idx, SCALE, workspace=torch.empty(need, device=DEV, dtype=torch.uint8))
+    _check(q, cache, idx, d_v, out, lse)
+    for o, l in (dsa.sparse_attn_kv4(q, *cache, idx, SCALE), dsa.sparse_attn(q, dsa.kv4_read(*cache, Lk), idx, d_v, SCALE)):
+        assert torch.equal(out, o) and torch.equal(lse, l)
+
+
 def test_rows_behind_four_gigabytes():
     q, kv, d_v, g = _inputs("mla", 2, 1, 64, 6)
     Lk = 9_000_000                                         # 2 x 2.3 GB of codes

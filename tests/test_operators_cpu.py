@@ -147,6 +147,19 @@ def test_kv4_workspace_holds_unpacked_rows_where_lists_repeat_them():
     assert size(dsa.OP_FORWARD_KV4, 1, 1, 4096, 2048, 128, 512) == size(dsa.OP_FORWARD, 1, 1, 4096, 2048, 128, 512) > 0
 
 
+def test_workspace_of_more_queries_than_cache_rows():
+    # the lists' length decides, not the rows that they name
+    for B, Lq, Lk, k in [(1, 4, 3, 2048), (2, 9, 1, 700), (1, 40, 39, 2048)]:
+        need = dsa.workspace_size(dsa.OP_SPARSE_ATTN, B, Lq, Lq, k, 128, 512)
+        assert dsa.workspace_size(dsa.OP_SPARSE_ATTN, B, Lq, Lk, k, 128, 512) == need
+        assert (need > 0) == (Lq < 40)                     # 40 rows of 16 tiles are not split
+    for k in (0, 2049):
+        assert dsa.workspace_size(dsa.OP_SPARSE_ATTN, 1, 4, 3, k, 128, 512) == 0
+    # these place query i at position Lk - Lq + i or later
+    for op in (dsa.OP_TOPK, dsa.OP_FORWARD, dsa.OP_FORWARD_LOWMEM, dsa.OP_INDEXER_TOPK, dsa.OP_WINDOW_ATTN, dsa.OP_FORWARD_KV4):
+        assert dsa.workspace_size(op, 1, 4, 3, 2048, 128, 512) == 0
+
+
 def test_window_attention_refuses(L):
     good = dsa.AttnArgs(128, 576, 512, 0.07, 16, 16)
     f = L.dsa_window_attn
