@@ -362,7 +362,8 @@ dsa_status dsa_sparse_attn_kv4(const dsa_kv4_attn_args *args, int B, int Lq, int
  * dsa_forward with the latent rows in the 4-bit cache (the indexer's keys stay e4m3).
  *   sel_scores: as dsa_forward_timed (may be NULL); workspace: as dsa_forward (DSA_OP_FORWARD
  *   or DSA_OP_FORWARD_LOWMEM), or DSA_OP_FORWARD_KV4 with the room that dsa_sparse_attn_kv4
- *   describes; short sequences as there.
+ *   describes, here for the first q_offset + Lq rows of each sequence, which are all that the
+ *   selection can name; short sequences as there.
  */
 dsa_status dsa_forward_kv4(const dsa_indexer_args *iargs, const dsa_kv4_attn_args *kargs, int k, int32_t *indices,
                            float *sel_scores, void *out, float *lse, void *workspace, size_t workspace_bytes,

@@ -427,13 +427,25 @@ dsa_status launch_attn_mode(AttnParams p, const void* q, const void* kv, int d_q
 // (64) 746 in the kernel, 621 unpacked; 128 over 4096 (64) 116, 102; 256 over 32768 (16) 293, 269;
 // 512 over 131072 (8) 452, 428; 256 over 131072 (4) 298, 297; the launch shows below 131072 named rows:
 // 64 over 4096 62, 60; 40 over 4096 68, 70; 300 over 300 with k = 256 57, 61.
-bool kv4_unpacks(int B, int Lq, int Lk, int k) {
-  const long long slots = (long long)B * Lq * (k < Lk ? k : Lk), rows = (long long)B * Lk;
+bool kv4_unpacks(long long slots, long long rows) {
   return slots >= 8 * rows + 131072 && rows + 1 < (1LL << 31);
 }
+// Cache rows of a sequence that the lists of queries q_offset .. q_offset + Lq - 1 can name, and
+// the entries of all lists: lists of the caller's (causal false) may name any row, those of the
+// forward pass hold the min(k, t + 1) positions up to each query's own t.
+struct Kv4Reach {
+  int rows;
+  long long slots;
+};
+Kv4Reach kv4_reach(int B, int Lq, int Lk, int q_offset, int k, bool causal) {
+  if (!causal) return {Lk, (long long)B * Lq * (k < Lk ? k : Lk)};
+  const long long full = (long long)q_offset + Lq - (k > q_offset + 1 ? k - 1 : q_offset);   // queries that see k keys
+  const long long n = full > 0 ? full : 0, rest = Lq - n;                                    // the others see t + 1
+  return {q_offset + Lq, (long long)B * (n * k + rest * q_offset + rest * (rest + 1) / 2)};
+}
 // Bytes behind the attention's own workspace that this takes: the rows and one of zeros.
-size_t kv4_unpack_bytes(int B, int Lq, int Lk, int k, int d_qk) {
-  return kv4_unpacks(B, Lq, Lk, k) ? 256 + ((size_t)B * Lk + 1) * d_qk * 2 : 0;
+size_t kv4_unpack_bytes(int B, const Kv4Reach& r, int d_qk) {
+  return kv4_unpacks(r.slots, (long long)B * r.rows) ? 256 + ((size_t)B * r.rows + 1) * d_qk * 2 : 0;
 }
 
 // Attention over the 4-bit cache; `dense_idx_out` as in run_attn.
@@ -441,13 +453,14 @@ dsa_status run_attn_kv4(const dsa_kv4_attn_args* a, int B, int Lq, int Lk, int q
                         const int32_t* idx, int k, void* out, float* lse, void* ws, size_t ws_bytes, cudaStream_t st,
                         int32_t* dense_idx_out = nullptr) {
   // Not for dense rows: their boxes take rows behind the query, which may hold a NaN.
-  const size_t unpack = dense_idx_out ? 0 : kv4_unpack_bytes(B, Lq, Lk, k, a->d_qk);
+  const Kv4Reach reach = kv4_reach(B, Lq, Lk, q_offset, k, compact);
+  const size_t unpack = dense_idx_out ? 0 : kv4_unpack_bytes(B, reach, a->d_qk);
   const size_t attn_need = attn_ws_bytes(B, Lq, k, a->H, a->d_v);
   if (unpack && ws && aligned16(ws) && ws_bytes >= attn_need + unpack) {
     char* rows = static_cast<char*>(ws) + round_up(attn_need, 256);
     Kv4Params r{};
-    r.div_l = fast_div((uint32_t)Lk);
-    r.B = B; r.L = Lk; r.Lk = Lk; r.d_qk = a->d_qk; r.d_v = a->d_v;
+    r.div_l = fast_div((uint32_t)reach.rows);
+    r.B = B; r.L = reach.rows; r.Lk = Lk; r.d_qk = a->d_qk; r.d_v = a->d_v;
     r.zero_rows = 1;
     r.out = reinterpret_cast<__nv_bfloat16*>(rows);
     r.codes = const_cast<uint8_t*>(reinterpret_cast<const uint8_t*>(a->codes));
@@ -455,7 +468,7 @@ dsa_status run_attn_kv4(const dsa_kv4_attn_args* a, int B, int Lq, int Lk, int q
     r.tail = const_cast<__nv_bfloat16*>(reinterpret_cast<const __nv_bfloat16*>(a->tail));
     if (launch_kv4_read(r, st) != cudaSuccess) return DSA_ERR_CUDA;
     const dsa_attn_args b{a->H, a->d_qk, a->d_v, a->scale, a->q, rows};
-    return run_attn(&b, B, Lq, Lk, q_offset, compact, idx, k, out, lse, ws, attn_need, st, nullptr, true);
+    return run_attn(&b, B, Lq, reach.rows, q_offset, compact, idx, k, out, lse, ws, attn_need, st, nullptr, true);
   }
   AttnParams p{};
   p.B = B; p.Lq = Lq; p.Lk = Lk; p.H = a->H; p.k = k;
@@ -780,7 +793,9 @@ size_t dsa_workspace_size_args(dsa_op op, const dsa_indexer_args* iargs, int k, 
       if (H <= 0 || d_v <= 0) return 0;
       return (op == DSA_OP_FORWARD_KV4 ? scores_ws_bytes(iargs) : 0) +
              attn_ws_bytes(iargs->B, iargs->Lq, k, H, d_v) +
-             kv4_unpack_bytes(iargs->B, iargs->Lq, iargs->Lk, k, d_v + kRopeDim);
+             kv4_unpack_bytes(iargs->B,
+                              kv4_reach(iargs->B, iargs->Lq, iargs->Lk, iargs->q_offset, k, op == DSA_OP_FORWARD_KV4),
+                              d_v + kRopeDim);
     }
     case DSA_OP_WINDOW_ATTN:
       break;
@@ -794,7 +809,9 @@ size_t dsa_workspace_size(dsa_op op, int B, int Lq, int Lk, int k, int H, int d_
   if (op == DSA_OP_SPARSE_ATTN || op == DSA_OP_SPARSE_ATTN_KV4)
     return k > kMaxK ? 0
                      : attn_ws_bytes(B, Lq, k, H, d_v) +
-                           (op == DSA_OP_SPARSE_ATTN_KV4 ? kv4_unpack_bytes(B, Lq, Lk, k, d_v + kRopeDim) : 0);
+                           (op == DSA_OP_SPARSE_ATTN_KV4
+                                ? kv4_unpack_bytes(B, kv4_reach(B, Lq, Lk, 0, k, false), d_v + kRopeDim)
+                                : 0);
   if (Lq > Lk) return 0;
   if (op == DSA_OP_WINDOW_ATTN) return attn_ws_bytes(B, Lq, k < Lk ? k : Lk, H, d_v);
   if (k > kMaxK) return 0;

@@ -215,6 +215,24 @@ def test_forward_over_unpacked_rows():
     _check(inp["q"], cache, got[0], wl.Dv, got[1], got[2], [0, 350, 699])
 
 
+@pytest.mark.parametrize("B,Lq,Lk,off", [(2, 1500, 6000, 900), (1, 700, 20000, 1400), (3, 40, 9000, 2100)])
+def test_forward_at_the_start_of_a_longer_cache(B, Lq, Lk, off):
+    # the rows behind q_offset + Lq - 1 hold nothing yet: none of them may count or be read
+    wl = WORKLOADS["prefill_8k"].with_(B=B, Lq=Lq, Lk=Lk, q_offset=off)
+    inp = make_inputs(wl, DEV, 1)
+    end = off + Lq
+    cache = _cache(inp["kv"], wl.Dv)
+    side = [inp[x] for x in ("q_I", "q_scale", "w", "k_I", "k_scale")]
+    short = side[:3] + [side[3][:, :end].contiguous(), side[4][:, :end].contiguous()]
+    want = dsa.forward_kv4(*short, inp["q"], *(t[:, :end].contiguous() for t in cache), wl.k, wl.scale, off)
+    cache[1][:, end:] = float("nan")
+    cache[2][:, end:] = float("nan")
+    for low in (False, True):
+        got = dsa.forward_kv4(*side, inp["q"], *cache, wl.k, wl.scale, off, low_memory=low)
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+    _check(inp["q"], cache, got[0], wl.Dv, got[1], got[2], [0, B * Lq // 2, B * Lq - 1])
+
+
 @pytest.mark.parametrize("shape", ["mla", "tiny"])
 @pytest.mark.parametrize("B,Lq,Lk,k", [(1, 4, 3, 2048), (2, 9, 1, 700)])
 def test_more_queries_than_cache_rows(shape, B, Lq, Lk, k):

@@ -147,6 +147,28 @@ def test_kv4_workspace_holds_unpacked_rows_where_lists_repeat_them():
     assert size(dsa.OP_FORWARD_KV4, 1, 1, 4096, 2048, 128, 512) == size(dsa.OP_FORWARD, 1, 1, 4096, 2048, 128, 512) > 0
 
 
+@pytest.mark.parametrize("B,Lq,Lk,off", [(1, 1024, 131072, 1500), (2, 1500, 6000, 900), (4, 2000, 4000, 2000),
+                                         (1, 1024, 131072, 130048)])
+def test_forward_workspace_holds_the_rows_that_can_be_selected(B, Lq, Lk, off):
+    ia = dsa.IndexerArgs(B, Lq, Lk, off, 64, 128, 16, None, 16, 16, None)
+    plain = dsa.workspace_size_args(dsa.OP_FORWARD, ia, 2048, 128, 512)
+    room = dsa.workspace_size_args(dsa.OP_FORWARD_KV4, ia, 2048, 128, 512) - plain
+    assert 0 <= room - (B * (off + Lq) + 1) * 576 * 2 <= 256
+    # lists of the caller's may name every row
+    any_ = dsa.workspace_size_args(dsa.OP_SPARSE_ATTN_KV4, ia, 2048, 128, 512)
+    assert any_ == dsa.workspace_size(dsa.OP_SPARSE_ATTN_KV4, B, Lq, Lk, 2048, 128, 512)
+
+
+def test_forward_workspace_counts_the_entries_that_lists_hold():
+    # 600 queries from position 0: t + 1 entries each, 180300 in all, over 600 rows of 131072;
+    # 20 queries from position 0: 210, too few to unpack 20 rows for, whatever k is
+    for Lq, unpacks in ((600, True), (20, False)):
+        ia = dsa.IndexerArgs(1, Lq, 131072, 0, 64, 128, 16, None, 16, 16, None)
+        room = dsa.workspace_size_args(dsa.OP_FORWARD_KV4, ia, 2048, 128, 512) - \
+            dsa.workspace_size_args(dsa.OP_FORWARD, ia, 2048, 128, 512)
+        assert (room > 0) == unpacks and room <= 256 + (Lq + 1) * 576 * 2
+
+
 def test_workspace_of_more_queries_than_cache_rows():
     # the lists' length decides, not the rows that they name
     for B, Lq, Lk, k in [(1, 4, 3, 2048), (2, 9, 1, 700), (1, 40, 39, 2048)]:
