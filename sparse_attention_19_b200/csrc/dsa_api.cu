@@ -422,13 +422,18 @@ dsa_status launch_attn_mode(AttnParams p, const void* q, const void* kv, int d_q
 
 // Whether the attention over the 4-bit cache unpacks the cache into the workspace and attends
 // over bf16 rows: when the lists name each row often enough.  Converting inside the attention
-// costs 0.06 ns more per named row than gathering bf16 rows (16 heads: 0.07); unpacking costs 0.4 ns
-// per cache row and a launch.  Both ways in us, 128 heads, k = 2048 (uses of a row): 1024 rows over 32768
-// (64) 746 in the kernel, 621 unpacked; 128 over 4096 (64) 116, 102; 256 over 32768 (16) 293, 269;
-// 512 over 131072 (8) 452, 428; 256 over 131072 (4) 298, 297; the launch shows below 131072 named rows:
-// 64 over 4096 62, 60; 40 over 4096 68, 70; 300 over 300 with k = 256 57, 61.
+// costs 0.06 ns more per named row than gathering bf16 rows (16 heads: 0.07 and more); unpacking costs
+// 0.3 ns per cache row and a launch, which shows in short calls: five uses of a row and 49152 entries on
+// top.  Both ways alone, caches cold, in us (in the kernel / unpacked), 128 heads, k = 2048:
+//   131072 rows: 256 queries 290/294, 320 303/300, | 384 358/347, 512 416/396, 640 527/493
+//   32768 rows:  64 queries 72/73, 96 124/122, | 112 123/116, 128 123/116, 256 271/253, 1024 749/626
+//   8192 rows:   24 queries 48/50, 32 52/50, | 48 66/62, 64 66/62
+//   4096 rows:   16 queries 39/41, 24 47/47, 32 49/49, | 40 61/59, 64 64/61, 128 117/105
+// ("|": the rule unpacks from there on).  16 heads: 131072 rows, 256 queries 130/120, | 512 217/179;
+// 32768 rows, 64 queries 37/38, | 128 66/60; 8192 rows, 24 queries 26/28, | 64 37/36; 4096 rows,
+// 16 queries 20/22, 32 27/27, | 40 33/33, 64 37/34.
 bool kv4_unpacks(long long slots, long long rows) {
-  return slots >= 8 * rows + 131072 && rows + 1 < (1LL << 31);
+  return slots >= 5 * rows + 49152 && rows + 1 < (1LL << 31);
 }
 // Cache rows of a sequence that the lists of queries q_offset .. q_offset + Lq - 1 can name, and
 // the entries of all lists: lists of the caller's (causal false) may name any row, those of the

@@ -159,6 +159,16 @@ def test_forward_workspace_holds_the_rows_that_can_be_selected(B, Lq, Lk, off):
     assert any_ == dsa.workspace_size(dsa.OP_SPARSE_ATTN_KV4, B, Lq, Lk, 2048, 128, 512)
 
 
+@pytest.mark.parametrize("Lk,below,above", [(131072, 256, 512), (32768, 64, 128), (8192, 24, 64), (4096, 24, 64)])
+def test_the_unpacking_rule_lies_between_what_was_measured(Lk, below, above):
+    # queries of 2048 entries for which converting in the kernel was no slower, and slower
+    def room(Lq):
+        return dsa.workspace_size(dsa.OP_SPARSE_ATTN_KV4, 1, Lq, Lk, 2048, 128, 512) - \
+            dsa.workspace_size(dsa.OP_SPARSE_ATTN, 1, Lq, Lk, 2048, 128, 512)
+
+    assert room(below) == 0 and room(above) >= (Lk + 1) * 576 * 2
+
+
 def test_forward_workspace_counts_the_entries_that_lists_hold():
     # 600 queries from position 0: t + 1 entries each, 180300 in all, over 600 rows of 131072;
     # 20 queries from position 0: 210, too few to unpack 20 rows for, whatever k is
