@@ -622,11 +622,12 @@ def _attn_outputs(q, d_v, out, lse, want_lse):
 
 
 def sparse_attn_kv4(q, codes, scales, tail, indices, scale, out=None, lse=None, want_lse=True, workspace=None,
-                    stream=None):
+                    stream=None, low_memory=False):
     """sparse_attn over the rows of a 4-bit cache (kv4_cache): bf16 [B, Lq, H, d_v] and fp32
     lse [B, Lq, H].  Rows that ``indices`` does not name may hold anything.  Without a
     ``workspace`` of the caller's, a prefill chunk takes one with room for the unpacked rows
-    (OP_SPARSE_ATTN_KV4); OP_SPARSE_ATTN bytes do, and are slower there."""
+    (OP_SPARSE_ATTN_KV4, 2.8 times the cache); with ``low_memory`` it takes OP_SPARSE_ATTN bytes,
+    the least that a caller may give, and is slower there.  The result is the same."""
     c, a = _kv4_attn_args(q, codes, scales, tail, scale)
     dev, Lq, k = q.device, q.shape[1], indices.shape[-1]
     _need_at(indices, torch.int32, (c.B, Lq, k), "indices", dev)
@@ -634,7 +635,8 @@ def sparse_attn_kv4(q, codes, scales, tail, indices, scale, out=None, lse=None, 
 
     def call(st):
         o, l = _attn_outputs(q, c.d_v, out, lse, want_lse)
-        ws, nbytes = _workspace(OP_SPARSE_ATTN_KV4, c.B, Lq, c.Lk, k, a.H, c.d_v, dev, workspace)
+        ws, nbytes = _workspace(OP_SPARSE_ATTN if low_memory else OP_SPARSE_ATTN_KV4, c.B, Lq, c.Lk, k, a.H, c.d_v,
+                                dev, workspace)
         _check(lib().dsa_sparse_attn_kv4(ctypes.byref(a), c.B, Lq, c.Lk, indices.data_ptr(), k, o.data_ptr(), _ptr(l),
                                          _ptr(ws), nbytes, st), "dsa_sparse_attn_kv4")
         return o, l

@@ -202,6 +202,27 @@ def test_unpacked_rows_two_calls_at_once_and_from_a_graph():
     assert torch.equal(o, want2[0]) and torch.equal(l, want2[1])
 
 
+@pytest.mark.parametrize("Lq,k", [(200, 1000), (5, 2048), (12, 2048)])
+def test_low_memory_takes_no_room_for_unpacked_rows(Lq, k):
+    # many rows: no workspace at all; few: the partial results of the splits
+    q, kv, d_v, g = _inputs("mla", 1, Lq, 20000 if Lq == 200 else 900, 23)
+    cache = _cache(kv, d_v)
+    Lk = kv.shape[1]
+    idx = _indices(g, 1, Lq, Lk, k, "prefix")
+    want = dsa.sparse_attn_kv4(q, *cache, idx, SCALE)
+    out, lse = torch.empty_like(want[0]), torch.empty_like(want[1])
+    least = dsa.workspace_size(dsa.OP_SPARSE_ATTN, 1, Lq, Lk, k, 128, 512)
+    assert (least > 0) == (Lq != 200)
+    torch.cuda.synchronize()
+    torch.cuda.reset_peak_memory_stats()
+    before = torch.cuda.memory_allocated()
+    dsa.sparse_attn_kv4(q, *cache, idx, SCALE, out=out, lse=lse, low_memory=True)
+    torch.cuda.synchronize()
+    # the allocator hands out blocks in steps of 2 MB at most
+    assert torch.cuda.max_memory_allocated() - before <= (least + (2 << 20) if least else 0)
+    assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
+
+
 def test_forward_over_unpacked_rows():
     wl = WORKLOADS["prefill_8k"].with_(B=1, Lq=700, Lk=4200, q_offset=3500)
     inp = make_inputs(wl, DEV, 1)
