@@ -236,7 +236,9 @@ def test_forward_over_unpacked_rows():
     _check(inp["q"], cache, got[0], wl.Dv, got[1], got[2], [0, 350, 699])
 
 
-@pytest.mark.parametrize("B,Lq,Lk,off", [(2, 1500, 6000, 900), (1, 700, 20000, 1400), (3, 40, 9000, 2100)])
+# the last three: every position is selected, with the keys of few rows split and of many not
+@pytest.mark.parametrize("B,Lq,Lk,off", [(2, 1500, 6000, 900), (1, 700, 20000, 1400), (3, 40, 9000, 2100),
+                                         (3, 1, 2500, 1499), (1, 4, 3000, 2044), (2, 300, 3000, 70)])
 def test_forward_at_the_start_of_a_longer_cache(B, Lq, Lk, off):
     # the rows behind q_offset + Lq - 1 hold nothing yet: none of them may count or be read
     wl = WORKLOADS["prefill_8k"].with_(B=B, Lq=Lq, Lk=Lk, q_offset=off)

@@ -83,3 +83,33 @@ def test_gradient_sums_take_every_row_once(B, L, H, D, nd, rs, F, inter, kind):
     assert torch.equal(dw.double(), (dy.double() * x.double())[..., :nd].sum((0, 1, 2)))
     if kind == "layer":
         assert torch.equal(db.double(), dy.double()[..., :nd].sum((0, 1, 2)))
+
+
+def test_rows_behind_four_gigabytes():
+    # 2.3e9 elements: byte and element offsets pass 32 bits in x, dy and every output
+    B, L, H, D = 2, 35500, 64, 512
+    g = torch.Generator(device=DEV).manual_seed(1)
+    row = torch.randn(B, 500, H, D, generator=g, device=DEV, dtype=torch.bfloat16)
+    dy_row = torch.randn(B, 500, H, D, generator=g, device=DEV, dtype=torch.bfloat16)
+    x, dy = (torch.empty(B, L, H, D, device=DEV, dtype=torch.bfloat16) for _ in range(2))
+    for i in range(0, L, 500):
+        x[:, i:i + 500], dy[:, i:i + 500] = row, dy_row
+    inv = (10000.0 ** (-torch.arange(64, device=DEV) / 64)).float()
+    w = 1 + 0.1 * torch.randn(D, generator=g, device=DEV)
+    pos = (torch.arange(L, device=DEV, dtype=torch.int32) % 500).expand(B, L).contiguous()   # every 500 rows again
+    how = dict(norm="rms", weight=w, rot_start=384)
+    y = dsa.norm_rope(x, inv, positions=pos, **how)
+    want = dsa.norm_rope(row, inv, positions=pos[:, :500].contiguous(), **how)
+    assert all(torch.equal(y[:, i:i + 500], want) for i in range(0, L, 500))
+    del y
+    codes, scale = dsa.norm_rope(x, inv, positions=pos, e4m3=True, **how)
+    wc, ws = dsa.norm_rope(row, inv, positions=pos[:, :500].contiguous(), e4m3=True, **how)
+    assert all(torch.equal(codes[:, i:i + 500].view(torch.uint8), wc.view(torch.uint8)) for i in range(0, L, 500))
+    assert all(torch.equal(scale[:, i:i + 500], ws) for i in range(0, L, 500))
+    del codes
+    dx, dw, _ = dsa.norm_rope_bwd(dy, x, inv, positions=pos, **how)
+    wx, ww, _ = dsa.norm_rope_bwd(dy_row, row, inv, positions=pos[:, :500].contiguous(), **how)
+    assert all(torch.equal(dx[:, i:i + 500], wx) for i in range(0, L, 500))
+    # 71 times the sums of one part: 4.5e6 terms of about 1, each sum at most 600 additions deep
+    size = (dy_row.double().abs().amax() * row.double().abs().amax() * 2)
+    assert ((dw.double() - 71 * ww.double()).abs() <= 1200 * 2.0 ** -24 * size * B * L * H).all()
