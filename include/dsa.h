@@ -76,7 +76,7 @@ typedef enum {
     DSA_OP_FORWARD = 2,          /* dsa_forward, staged selection (the faster path) */
     DSA_OP_INDEXER_TOPK = 3,
     DSA_OP_FORWARD_LOWMEM = 4,   /* dsa_forward, fused selection (no score matrix) */
-    DSA_OP_WINDOW_ATTN = 5,      /* dsa_window_attn; k = window + sinks (of any size) */
+    DSA_OP_WINDOW_ATTN = 5,      /* dsa_window_attn; k = window + sinks, or INT_MAX where that is less */
     DSA_OP_SPARSE_ATTN_KV4 = 6,  /* dsa_sparse_attn_kv4 with room to unpack the cache where that is faster */
     DSA_OP_FORWARD_KV4 = 7       /* dsa_forward_kv4, staged selection and the same room */
 } dsa_op;
@@ -262,7 +262,8 @@ dsa_status dsa_indexer_kl_loss_selected(const dsa_attn_args *args, int B, int Lq
  *       (rot_start + j, rot_start + n_freq + j), or (rot_start + 2j, rot_start + 2j + 1)
  *       when interleaved.  The angle is reduced in 64 bits, so far positions are exact.
  * x may be a slice of a wider buffer (strides in elements, columns contiguous); a stride
- * of 0 reads the same rows again.  D, norm_dim, rot_start, the strides: multiples of 8;
+ * of 0 reads the same rows again.  Nothing is recorded for a gradient: dsa_norm_rope_bwd is
+ * called with the same arguments.  D, norm_dim, rot_start, the strides: multiples of 8;
  * n_freq: a multiple of 8; 8 <= D <= 1024.  B * L and B * L * H below 2^31.
  */
 typedef enum { DSA_NORM_NONE = 0, DSA_NORM_RMS = 1, DSA_NORM_LAYER = 2 } dsa_norm;

@@ -13,9 +13,10 @@
 //   g = dz w;  dx = r (g - xhat mean(g xhat) [- mean(g): layer norm]),  dx = dz behind
 //   norm_dim;  dw = sum over rows of dz xhat,  db = sum of dz.
 //
-// Both are bound by HBM (2 bytes read and 1 or 2 written per element; gradient: 4 read, 2
-// written), but at these widths only if the arithmetic stays below ~70 issued
-// instructions per 8 elements, so:
+// What cannot be done without is HBM traffic (2 bytes read and 1 or 2 written per element;
+// gradient: 4 read, 2 written).  At these widths it sets the pace only if the arithmetic stays
+// below ~70 issued instructions per 8 elements: the bf16 form and the gradient come to 0.86 and
+// 0.72 of the copy rate, e4m3 (whose kernel's comment has the reason) to 0.62.  So:
 //   * G lanes hold a head row in 16-byte vectors, and a lane holds BOTH vectors of a rotated
 //     pair (NP pair slots, NM slots for the columns that are not rotated): the rotation needs no
 //     exchange between lanes and every column is normalised once;
@@ -408,11 +409,13 @@ __global__ void __launch_bounds__(kThreads, resident(2 * NP + NM, LAYER)) norm_r
 }
 
 // e4m3 output.  A step holds whole tokens, a row per group of lanes in registers; its one
-// barrier completes the tokens' maxima.  Bound by issue slots (62 %) and the load/store pipe
-// (60 %) alike, 0.64 of the copy rate at 8192 x 64 x 128 (48 us): weights and angles come
-// from shared memory for every row, since holding them in registers costs more in warps (53
-// registers: four blocks an SM; the weights in registers 63-70 us, two rows per group with
-// one weight read 64 us, five blocks 54 us).
+// barrier completes the tokens' maxima.  0.62 of the copy rate at 8192 x 64 x 128 (49.6 us among
+// other passes, 48.0 with codes from one rounded reciprocal).  No pipe is full there (issue slots
+// 61 %, load/store pipe 58 %): nothing is in flight behind a step, so its warps wait for their own
+// rows, for weights and angles from shared memory and at the barrier, and the other three blocks of
+// the SM cover only part of that.  Weights and angles come from shared memory for every row,
+// since holding them in registers costs more in warps (56 registers: four blocks an SM; the
+// weights in registers 63-70 us, two rows per group with one weight read 64 us, five blocks 54 us).
 template <int G, int NP, int NM, bool FULL, bool LAYER>
 __global__ void __launch_bounds__(kThreads, resident_e4m3(2 * NP + NM, LAYER)) norm_rope_e4m3_kernel(const NormRopeParams p) {
   using S = Slots<G, NP, NM, FULL>;
@@ -546,9 +549,12 @@ __global__ void __launch_bounds__(kThreads) norm_rope_wide_kernel(const NormRope
 
 // Gradient.  Each block keeps the sums for dw and db of its columns in registers over all its
 // steps and leaves one partial row; a second kernel adds the partial rows in block
-// order, so the result does not depend on timing.  0.73 of the copy rate at 4096 x 64 x 128 (42
-// us): the running sums take registers (127), so 16 warps an SM have to cover the loads.  Two
-// blocks an SM in one wave: twice as many blocks in two waves took 47 us.
+// order, so the result does not depend on timing.  0.72 of the copy rate at 4096 x 64 x 128 (42.6
+// us): the running sums take registers (RMS norm: 127), so 16 warps an SM have to cover the loads.
+// Two blocks an SM in one wave: twice as many blocks in two waves took 47 us.  The layer norm's
+// db takes 32 registers more than the 128 of two blocks an SM leave: it spills 196 bytes (rows that
+// do not fill every slot: 248; widths of six to eight slots run one block, <32,2,4> at 255
+// registers with 444 bytes), 13.8 us in this kernel and 8.8 in the second for 16382 keys, caches cold.
 template <int G, int NP, int NM, bool FULL, bool LAYER>
 __global__ void __launch_bounds__(kThreads, (2 * NP + NM) > 4 ? 1 : 2) norm_rope_bwd_kernel(const NormRopeParams p) {
   using S = Slots<G, NP, NM, FULL>;

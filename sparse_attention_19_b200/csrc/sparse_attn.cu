@@ -45,16 +45,17 @@
 //
 // The kernel has two more forms that differ in where the keys come from (AttnMode below):
 //   * a sliding window and sinks (kWindow): the slots of a row are computed, not listed; 16
-//     slots that are consecutive rows come in one box (72 TMA requests a tile instead of 272), a group
+//     slots that are consecutive rows come in one box (68 TMA requests a tile and CTA instead of 272), a group
 //     with the seam or the end of the row by gathers.  Rows past the query or between the sinks
 //     and the window are never loaded, since a zero probability times a NaN would still
-//     reach the output.  4096 rows x (512 + 16) slots 735 us (819 TFLOP/s on the slots, 0.50 of the
-//     bf16 peak); bound by the chain S -> softmax -> P.V over only five tiles per row, the
-//     last of them one eighth full.
+//     reach the output.  4096 rows x (512 + 16) slots 857 us among other passes (703 TFLOP/s on the
+//     slots, 0.43 of the bf16 burst peak), 735 alone at burst clocks (0.50); bound by the chain
+//     S -> softmax -> P.V over only five tiles per row, the last of them one eighth full.
 //   * rows of the 4-bit cache (kPacked): 16 warps convert codes to bf16 planes in shared
 //     memory, in the layouts TMA writes for bf16 rows, once as key chunks and once as
 //     value stages.  Everything behind the operands is shared, so the result equals the bf16
-//     kernel's over the values that the cache holds bit for bit.  Meant for rows used a few times
+//     kernel's over the values that the cache holds bit for bit.  64 rows x 2048 68 us (bf16 rows 65:
+//     the cache saves memory, not time).  Meant for rows used a few times
 //     (decode); a chunk of queries that use each row many times has the cache unpacked first and runs
 //     kSelected, with masked slots gathering a row of zeros (the host's rule has the figures).
 #include <cuda.h>
@@ -266,8 +267,8 @@ __device__ __forceinline__ void store_codes(uint8_t* row, uint32_t lo, uint32_t 
 // columns of both chunks to a lane and row.  The registers that held a job's codes are
 // loaded again for the next tile as soon as it is converted, so a tile of loads is in
 // flight across units too.
-// What sets the pace is the converting warps' instruction stream: without the conversions'
-// arithmetic 861 -> 682 us (1024 rows x 2048 keys), without their loads 726, without their
+// What sets the pace is the converting warps' instruction stream (times alone at burst clocks):
+// without the conversions' arithmetic 861 -> 682 us (1024 rows x 2048 keys), without their loads 726, without their
 // stores no gain, without all three 420.  So: one wait and one fence per job, not per chunk (822),
 // the two chunks of a job in a rolled loop, since 24 warps in five roles also wait for
 // instructions (754 -> 734); all eight warps in every chunk (986), one more team of key
@@ -1003,7 +1004,10 @@ sparse_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
         }
         if (need) m = m_new;
         // Probabilities 2^(z*scale*log2e - m), packed to bf16 straight into P (row h of
-        // this lane's key-half plane, 128-byte swizzle); the row sum is kept in fp32.
+        // this lane's key-half plane, 128-byte swizzle); the row sum is kept in fp32.  The
+        // product with the bf16 values takes bf16 (both operands of an MMA have one type):
+        // every probability is off by at most 2^-8 of itself, which makes the output's
+        // error 2.1e-3 of its size where its own rounding alone leaves 1.7e-3.
         uint8_t* prow = p_sm + (pbuf * 2 + half) * kPlane64 + (h >> 3) * 1024 + (h & 7) * 128;
         const float2 scl = make_float2(p.scale_log2, p.scale_log2);
         const float2 nm = make_float2(-m_use, -m_use);
