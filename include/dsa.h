@@ -387,7 +387,7 @@ dsa_status dsa_window_attn(const dsa_attn_args *args, int B, int Lq, int Lk, int
 
 /*
  * Bytes of device workspace the entry point `op` needs for these sizes (0 = none).
- * For DSA_OP_FORWARD, DSA_OP_FORWARD_LOWMEM and DSA_OP_INDEXER_TOPK it assumes
+ * For DSA_OP_FORWARD, DSA_OP_FORWARD_LOWMEM, DSA_OP_FORWARD_KV4 and DSA_OP_INDEXER_TOPK it assumes
  * H_I = 64, d_I = 128 and q_offset = Lk - Lq (decode, or a prefill chunk);
  * dsa_workspace_size_args gives the exact figure for any indexer arguments.
  * DSA_OP_FORWARD includes the fp32 score matrix, B * Lq * Lk * 4 bytes (4.3 GB

@@ -317,7 +317,8 @@ struct Walk {
 // by less than 2^-44 of itself.  The product's one rounding then gives the rounded quotient
 // unless that lies so close to the middle of two floats, which no fp32 value over 448 and no bf16
 // value over an fp32 one does: a quotient on the border of two codes stays there.  (The
-// bare product with one float crosses it for 1 in 1000 pairs of bf16 significands.)
+// bare product with one float crosses it for 1 in 1000 pairs of bf16 significands.  Above
+// amax = 2^118 the second float is subnormal and the sum off by up to 2^-31: exact borders stay.)
 // Infinities take no second float (inf - inf, 0 * inf): with an infinite scale, finite
 // values become 0 and the infinite ones NaN.
 __device__ __forceinline__ float scale_of(float amax) {
